@@ -38,6 +38,8 @@ PATH_NO_FUSED = 0x400
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _Z = ctypes.c_size_t
+_L = ctypes.c_int64
+_F = ctypes.c_float
 SIGNATURES = {
     "dqg_abi_version": (_I, []),
     "dqg_status_string": (ctypes.c_char_p, [_I]),
@@ -59,6 +61,14 @@ SIGNATURES = {
     "packed_gemv_int4_prepack_sizes": (_I, [_I, _I, _I, ctypes.POINTER(_Z), ctypes.POINTER(_Z)]),
     "packed_gemv_int4_prepack": (_I, [_P, _P, _I, _I, _I, _P, _P, _P]),
     "packed_gemv_int4_tiled": (_I, [_P, _I, _I, _I, _P, _P, _I, _P, _P, _Z, _P]),
+    "kv4_page_bytes": (_Z, [_I, _I, _I, _I]),
+    "kv4_write": (_I, [_P, _P, _I, _L, _L, _I, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _P,
+                       _P]),
+    "kv4_read": (_I, [_P, _P, _I, _L, _L, _I, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _P,
+                      _P]),
+    "kv4_attention_workspace_bytes": (_Z, [_I, _I, _I, _I, _I, _I]),
+    "kv4_attention": (_I, [_P, _I, _L, _I, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I,
+                           _I, _I, _I, _P, _L, _P, _P, _P, _Z, _P]),
     "packed_dequant_f32": (_I, [_P, _P, _I, _I, _I, _I, _P, _P]),
     "dqg_stream_read": (_I, [_P, _Z, _P, _P]),
 }
@@ -384,6 +394,172 @@ def packed_gemv_int4_tiled(x, w_tiled, s_tiled, N: int, group: int, y=None,
         _ptr(x), T, K, N, _ptr(w_tiled), _ptr(s_tiled), group, _ptr(y), _ptr(workspace),
         0 if workspace is None else workspace.numel(), _stream(x)))
     return y
+
+
+# ---- 4-bit key/value cache ---------------------------------------------------------------
+def kv4_page_bytes(kv_heads: int, head_dim: int, page_size: int, group: int) -> int:
+    return int(LIB.kv4_page_bytes(kv_heads, head_dim, page_size, group))
+
+
+def kv4_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int, group: int,
+              device) -> torch.Tensor:
+    """A cache of num_pages empty pages, uint8 [num_pages, page bytes]."""
+    n = kv4_page_bytes(kv_heads, head_dim, page_size, group)
+    if n == 0:
+        raise ValueError("unsupported cache sizes")
+    return torch.zeros((num_pages, n), dtype=torch.uint8, device=device)
+
+
+def _need_rows(t: torch.Tensor, name: str, T: int, heads: int, D: int, device):
+    """bf16 [T, heads, D] whose rows may be columns of a wider matrix: only the row stride is
+    free.  Returns it."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
+        raise TypeError(f"{name} must be bf16 (or its 16-bit patterns), got {t.dtype}")
+    if t.shape != (T, heads, D):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, heads, D)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != D):
+        raise ValueError(f"{name}: heads and dims of a row must be contiguous")
+    return s0 if T > 1 else max(s0, heads * D)
+
+
+def _need_i32(t: torch.Tensor, name: str, shape, device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _kv4_where(cu_rows, kv_lens, block_table, cache, kv_heads, D, page_size, group, status):
+    """Checks what the cache calls share; returns (device, B, max_pages, num_pages)."""
+    if not isinstance(cache, torch.Tensor):
+        raise TypeError("cache must be a torch.Tensor")
+    dev = cache.device
+    if dev.type != "cuda":
+        raise ValueError("cache must be a device tensor")
+    n = LIB.kv4_page_bytes(kv_heads, D, page_size, group)
+    if n == 0:
+        raise ValueError(f"unsupported cache sizes: {kv_heads} heads of {D}, pages of {page_size}, "
+                         f"group {group}")
+    if cache.dtype != torch.uint8 or cache.dim() != 2 or cache.shape[1] != n:
+        raise ValueError(f"cache must be uint8 [pages, {n}], got {cache.dtype} "
+                         f"{tuple(cache.shape)}")
+    if not cache.is_contiguous():
+        raise ValueError("cache must be contiguous")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be an int32 tensor [B, max_pages]")
+    B, max_pages = block_table.shape
+    _need_i32(block_table, "block_table", (B, max_pages), dev)
+    _need_i32(cu_rows, "cu_rows", (B + 1,), dev)
+    _need_i32(kv_lens, "kv_lens", (B,), dev)
+    if status is not None:
+        _need_i32(status, "status", (1,), dev)
+    return dev, B, max_pages, cache.shape[0]
+
+
+def _call(fn: str, device, *args):
+    """Calls an entry point on the device's current stream, with the device current."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        rc = getattr(LIB, fn)(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = getattr(LIB, fn)(*args, stream)
+    if rc != DQG_OK:
+        raise DqgError(fn, rc)
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def kv4_write(k, v, cu_rows, kv_lens, block_table, cache, page_size: int, group: int, fmt: int,
+              status=None) -> None:
+    """Quantises the rows k, v (bf16 [T, kv_heads, head_dim], rows may be strided) into their
+    places in ``cache`` (see ``kv4_cache``); cu_rows int32 [B + 1], kv_lens int32 [B] lengths with
+    these rows, block_table int32 [B, max_pages], status int32 [1] or None."""
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a tensor [T, kv_heads, head_dim]")
+    T, H, D = k.shape
+    dev, B, mp, pages = _kv4_where(cu_rows, kv_lens, block_table, cache, H, D, page_size, group,
+                                   status)
+    ks = _need_rows(k, "k", T, H, D, dev)
+    vs = _need_rows(v, "v", T, H, D, dev)
+    _call("kv4_write", dev, k.data_ptr(), v.data_ptr(), T, ks, vs, B, cu_rows.data_ptr(),
+          kv_lens.data_ptr(), block_table.data_ptr(), mp, cache.data_ptr(), pages, H, D, page_size,
+          group, fmt, _addr(status))
+
+
+def kv4_read(T: int, kv_heads: int, head_dim: int, cu_rows, kv_lens, block_table, cache,
+             page_size: int, group: int, fmt: int, k=None, v=None,
+             status=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The T rows' keys and values back from the cache, bf16 [T, kv_heads, head_dim] each (k and v
+    are allocated when not given; rows behind the last sequence are left as they are)."""
+    dev, B, mp, pages = _kv4_where(cu_rows, kv_lens, block_table, cache, kv_heads, head_dim,
+                                   page_size, group, status)
+    if k is None:
+        k = torch.empty((T, kv_heads, head_dim), dtype=torch.bfloat16, device=dev)
+    if v is None:
+        v = torch.empty((T, kv_heads, head_dim), dtype=torch.bfloat16, device=dev)
+    ks = _need_rows(k, "k", T, kv_heads, head_dim, dev)
+    vs = _need_rows(v, "v", T, kv_heads, head_dim, dev)
+    _call("kv4_read", dev, k.data_ptr(), v.data_ptr(), T, ks, vs, B, cu_rows.data_ptr(),
+          kv_lens.data_ptr(), block_table.data_ptr(), mp, cache.data_ptr(), pages, kv_heads,
+          head_dim, page_size, group, fmt, _addr(status))
+    return k, v
+
+
+def kv4_attention_workspace_bytes(T: int, B: int, heads: int, kv_heads: int, head_dim: int,
+                                  max_kv_len: int) -> int:
+    return int(LIB.kv4_attention_workspace_bytes(T, B, heads, kv_heads, head_dim, max_kv_len))
+
+
+def kv4_workspace(T: int, B: int, heads: int, kv_heads: int, head_dim: int, max_kv_len: int,
+                  device) -> Optional[torch.Tensor]:
+    """Scratch for kv4_attention calls of up to these sizes, or None where none is needed."""
+    n = kv4_attention_workspace_bytes(T, B, heads, kv_heads, head_dim, max_kv_len)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def kv4_attention(q, cu_rows, kv_lens, block_table, cache, kv_heads: int, page_size: int,
+                  group: int, fmt: int, scale: float, window: int = 0, sinks: int = 0,
+                  max_rows: int = 0, max_kv_len: int = 0, out=None, lse=None, workspace=None,
+                  status=None) -> torch.Tensor:
+    """Causal attention of the rows q (bf16 [T, heads, head_dim], rows may be strided) over the
+    cached keys and values, with an optional sliding window whose first ``sinks`` positions stay
+    visible; lse: fp32 [T, heads] to receive the log-sum-exp of the scores.  max_rows and
+    max_kv_len bound the sequences' rows and lengths where the caller knows them (0: unknown); they
+    choose the launch shape only.  workspace: ``kv4_workspace`` (None: caches are not split)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [T, heads, head_dim]")
+    T, H, D = q.shape
+    dev, B, mp, pages = _kv4_where(cu_rows, kv_lens, block_table, cache, kv_heads, D, page_size,
+                                   group, status)
+    qs = _need_rows(q, "q", T, H, D, dev)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+    os_ = _need_rows(out, "out", T, H, D, dev)
+    if lse is not None:
+        if lse.dtype != torch.float32:
+            raise TypeError(f"lse must be float32, got {lse.dtype}")
+        _need(lse, "lse", 4, (T, H), dev)
+    if workspace is not None:
+        _need(workspace, "workspace", 1, None, dev)
+    _call("kv4_attention", dev, q.data_ptr(), T, qs, B, cu_rows.data_ptr(), kv_lens.data_ptr(),
+          block_table.data_ptr(), mp, cache.data_ptr(), pages, H, kv_heads, D, page_size, group,
+          fmt, scale, window, sinks, max_rows, max_kv_len, out.data_ptr(), os_, _addr(lse),
+          _addr(status), _addr(workspace), 0 if workspace is None else workspace.numel())
+    return out
 
 
 def packed_dequant_f32(w, s, group: int, fmt: int, out=None) -> torch.Tensor:

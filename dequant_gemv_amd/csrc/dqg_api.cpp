@@ -299,6 +299,85 @@ bool gemv_sizes_ok(int T, int K, int N, int group) {
   return true;
 }
 
+// ---- 4-bit key/value cache -------------------------------------------------------------------
+constexpr int kKv4MaxT = 1 << 22;
+constexpr int kKv4MaxB = 65536;
+constexpr int kKv4MaxHeads = 1024;
+// workgroups of the attention kernel that a call is split into, at least, where the cache is
+// long enough
+constexpr int kKv4TargetWgs = 1024;
+constexpr int kKv4MinSplitSteps = 8;  // steps of a split, at least: two for each wavefront
+
+inline bool kv4_heads_ok(int Hkv, int D) {
+  return Hkv >= 1 && Hkv <= kKv4MaxHeads && (D == 64 || D == 128 || D == 256);
+}
+inline bool kv4_page_ok(int D, int page_size, int group) {
+  return (group == 32 || group == 128) && D % group == 0 && page_size >= 32 &&
+         page_size <= 65536 && (page_size & (page_size - 1)) == 0;
+}
+inline int log2_of(int v) { return 31 - __builtin_clz((unsigned)v); }
+
+struct Kv4Plan {
+  int nt, slots, S;
+  size_t part_bytes;  // of one split of one slot and head
+};
+// rows: rows of a sequence at most; steps: steps of a row tile at most
+Kv4Plan plan_kv4(int T, int B, int Hq, int Hkv, int D, int rows, long long steps) {
+  const int r = Hq / Hkv;
+  Kv4Plan p{};
+  rows = std::max(std::min(rows, T), (T + B - 1) / B);
+  const long long heads_rows = (long long)rows * r;
+  // one 16-row tile holds a token's heads; more rows share the decoded keys and values
+  p.nt = heads_rows <= 16 ? 1 : heads_rows <= 32 || D > 128 ? 2 : 4;
+  const int R = 16 * p.nt;
+  p.slots = (int)((long long)T * r / R) + B;
+  p.part_bytes = sizeof(float) * dqg::kv4_part_floats(p.nt, D);
+  const long long tiles = std::min<long long>(p.slots, B * ((heads_rows + R - 1) / R)) * Hkv;
+  p.S = 1;
+  if (tiles < kKv4TargetWgs)
+    p.S = (int)std::max(1LL, std::min((kKv4TargetWgs + tiles - 1) / tiles,
+                                      steps / kKv4MinSplitSteps));
+  return p;
+}
+long long kv4_steps(long long positions) {
+  return (positions + dqg::KV4_STEP - 1) / dqg::KV4_STEP;
+}
+bool kv4_attn_sizes_ok(int T, int B, int Hq, int Hkv, int D) {
+  return T >= 1 && T <= kKv4MaxT && B >= 1 && B <= kKv4MaxB && kv4_heads_ok(Hkv, D) && Hq >= 1 &&
+         Hq % Hkv == 0 && Hq <= 65536 && (long long)T * Hq < (1LL << 30);
+}
+
+int check_kv4_where(int T, int B, const int32_t* cu, const int32_t* lens, const int32_t* table,
+                    int max_pages, const uint8_t* cache, int num_pages, int Hkv, int D,
+                    int page_size, int group, int format, const int* status) {
+  if (!cu || !lens || !table || !cache) return DQG_ERR_INVALID_ARG;
+  if (T < 1 || B < 1 || max_pages < 1 || num_pages < 1 || Hkv < 1) return DQG_ERR_INVALID_ARG;
+  if (format != DQG_FMT_INT4 && format != DQG_FMT_FP4_E2M1) return DQG_ERR_UNSUPPORTED;
+  if (T > kKv4MaxT || B > kKv4MaxB || !kv4_heads_ok(Hkv, D) || !kv4_page_ok(D, page_size, group))
+    return DQG_ERR_UNSUPPORTED;
+  if ((long long)max_pages * page_size > (1LL << 30)) return DQG_ERR_UNSUPPORTED;
+  if (!aligned16(cache) || ((uintptr_t)cu & 3u) || ((uintptr_t)lens & 3u) ||
+      ((uintptr_t)table & 3u) || ((uintptr_t)status & 3u))
+    return DQG_ERR_MISALIGNED;
+  return DQG_OK;
+}
+int check_kv4_rows(const void* p, int64_t stride, int heads, int D) {
+  if (!p) return DQG_ERR_INVALID_ARG;
+  if (stride < (int64_t)heads * D || stride > ((int64_t)1 << 32)) return DQG_ERR_INVALID_ARG;
+  return aligned16(p) && stride % 8 == 0 ? DQG_OK : DQG_ERR_MISALIGNED;
+}
+dqg::Kv4Where kv4_where(int T, int B, const int32_t* cu, const int32_t* lens, const int32_t* table,
+                        int max_pages, const uint8_t* cache, int num_pages, int Hkv, int D,
+                        int page_size, int group, int* status) {
+  dqg::Kv4Where w{};
+  w.cu = cu; w.lens = lens; w.table = table; w.cache = const_cast<uint8_t*>(cache);
+  w.status = status; w.T = T; w.B = B; w.max_pages = max_pages; w.num_pages = num_pages;
+  w.Hkv = Hkv; w.page_shift = log2_of(page_size); w.group_shift = log2_of(group);
+  w.head_bytes = page_size * (D + 4 * D / group);
+  w.page_bytes = (int64_t)Hkv * w.head_bytes;
+  return w;
+}
+
 // ---- allocation-free GEMV: library-owned split-partial scratch -----------------------------
 // [error word, 256 bytes][split partials], one copy per GPU (a device global: it is zero-filled
 // when the code object loads, and every completed call leaves its partials zero again).
@@ -601,6 +680,102 @@ int packed_gemv_int4_tiled(const uint16_t* x, int T, int K, int N, const uint8_t
     g.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256);
   }
   return dqg::launch_gemv_tiled(g, stream) == hipSuccess ? DQG_OK : DQG_ERR_HIP;
+}
+
+size_t kv4_page_bytes(int Hkv, int D, int page_size, int group) {
+  if (!kv4_heads_ok(Hkv, D) || !kv4_page_ok(D, page_size, group)) return 0;
+  return (size_t)Hkv * page_size * (D + 4 * D / group);
+}
+
+int kv4_write(const uint16_t* k, const uint16_t* v, int T, int64_t k_stride, int64_t v_stride,
+              int B, const int32_t* cu_rows, const int32_t* kv_lens, const int32_t* block_table,
+              int max_pages, uint8_t* cache, int num_pages, int Hkv, int D, int page_size,
+              int group, int format, int* status, hipStream_t stream) {
+  int rc = check_kv4_where(T, B, cu_rows, kv_lens, block_table, max_pages, cache, num_pages, Hkv,
+                           D, page_size, group, format, status);
+  if (rc == DQG_OK) rc = check_kv4_rows(k, k_stride, Hkv, D);
+  if (rc == DQG_OK) rc = check_kv4_rows(v, v_stride, Hkv, D);
+  if (rc != DQG_OK) return rc;
+  dqg::Kv4RowsArgs a{};
+  a.w = kv4_where(T, B, cu_rows, kv_lens, block_table, max_pages, cache, num_pages, Hkv, D,
+                  page_size, group, status);
+  a.k = k; a.v = v; a.k_stride = k_stride; a.v_stride = v_stride;
+  return dqg::launch_kv4_write(a, D, format, stream) == hipSuccess ? DQG_OK : DQG_ERR_HIP;
+}
+
+int kv4_read(uint16_t* k, uint16_t* v, int T, int64_t k_stride, int64_t v_stride, int B,
+             const int32_t* cu_rows, const int32_t* kv_lens, const int32_t* block_table,
+             int max_pages, const uint8_t* cache, int num_pages, int Hkv, int D, int page_size,
+             int group, int format, int* status, hipStream_t stream) {
+  int rc = check_kv4_where(T, B, cu_rows, kv_lens, block_table, max_pages, cache, num_pages, Hkv,
+                           D, page_size, group, format, status);
+  if (rc == DQG_OK) rc = check_kv4_rows(k, k_stride, Hkv, D);
+  if (rc == DQG_OK) rc = check_kv4_rows(v, v_stride, Hkv, D);
+  if (rc != DQG_OK) return rc;
+  dqg::Kv4RowsArgs a{};
+  a.w = kv4_where(T, B, cu_rows, kv_lens, block_table, max_pages, cache, num_pages, Hkv, D,
+                  page_size, group, status);
+  a.k_out = k; a.v_out = v; a.k_stride = k_stride; a.v_stride = v_stride;
+  return dqg::launch_kv4_read(a, D, format, stream) == hipSuccess ? DQG_OK : DQG_ERR_HIP;
+}
+
+size_t kv4_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int max_kv_len) {
+  if (!kv4_attn_sizes_ok(T, B, Hq, Hkv, D) || max_kv_len < 1 || max_kv_len > (1 << 30)) return 0;
+  // a call's slots * Hkv * S is below 4 kKv4TargetWgs (it splits where its tiles, at least half
+  // the slots, are fewer than kKv4TargetWgs) and below slots * Hkv * steps / kKv4MinSplitSteps; the
+  // largest over the tile heights is monotonic in T, B and max_kv_len
+  size_t most = 0;
+  for (int nt = 1; nt <= (D > 128 ? 2 : 4); nt *= 2) {
+    const long long slots = (long long)T * (Hq / Hkv) / (16 * nt) + B;
+    const long long S = kv4_steps(max_kv_len) / kKv4MinSplitSteps;
+    if (S < 2) continue;
+    const long long parts = std::min(slots * Hkv * S, 4LL * kKv4TargetWgs);
+    most = std::max(most, (size_t)parts * sizeof(float) * dqg::kv4_part_floats(nt, D));
+  }
+  return up256(most);
+}
+
+int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32_t* cu_rows,
+                  const int32_t* kv_lens, const int32_t* block_table, int max_pages,
+                  const uint8_t* cache, int num_pages, int Hq, int Hkv, int D, int page_size,
+                  int group, int format, float scale, int window, int sinks, int max_rows,
+                  int max_kv_len, uint16_t* out, int64_t out_stride, float* lse, int* status,
+                  void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  int rc = check_kv4_where(T, B, cu_rows, kv_lens, block_table, max_pages, cache, num_pages, Hkv,
+                           D, page_size, group, format, status);
+  if (rc != DQG_OK) return rc;
+  if (Hq < 1 || Hq % Hkv || !std::isfinite(scale) || window < 0 || sinks < 0 || max_rows < 0 ||
+      max_kv_len < 0)
+    return DQG_ERR_INVALID_ARG;
+  if (!kv4_attn_sizes_ok(T, B, Hq, Hkv, D)) return DQG_ERR_UNSUPPORTED;
+  rc = check_kv4_rows(q, q_stride, Hq, D);
+  if (rc == DQG_OK) rc = check_kv4_rows(out, out_stride, Hq, D);
+  if (rc != DQG_OK) return rc;
+  if ((uintptr_t)lse & 3u) return DQG_ERR_MISALIGNED;
+  if (workspace && !aligned16(workspace)) return DQG_ERR_MISALIGNED;
+  const int cap = max_pages * page_size;
+  const int most = max_kv_len ? std::min(max_kv_len, cap) : cap;
+  if (workspace && workspace_bytes < kv4_attention_workspace_bytes(T, B, Hq, Hkv, D, most))
+    return DQG_ERR_WORKSPACE;
+  const int rows = max_rows ? max_rows : T;
+  long long steps = kv4_steps(most);
+  if (window > 0)  // a tile of up to 64 rows sees `window` positions a row and the first ones
+    steps = std::min(steps, kv4_steps((long long)window + 64) + 1 + kv4_steps(sinks));
+  const Kv4Plan p = plan_kv4(T, B, Hq, Hkv, D, rows, steps);
+  dqg::Kv4AttnArgs a{};
+  a.w = kv4_where(T, B, cu_rows, kv_lens, block_table, max_pages, cache, num_pages, Hkv, D,
+                  page_size, group, status);
+  a.q = q; a.q_stride = q_stride; a.out = out; a.out_stride = out_stride; a.lse = lse;
+  a.part = static_cast<float*>(workspace);
+  a.Hq = Hq; a.r = Hq / Hkv; a.scale = scale; a.window = window; a.sinks = sinks;
+  a.n_slots = p.slots; a.nt = p.nt;
+  a.S = 1;
+  if (workspace)  // (the query's bound; no call splits further than its workspace reaches)
+    a.S = (int)std::max<long long>(
+        1, std::min<long long>(p.S, (long long)(workspace_bytes / p.part_bytes) /
+                                        ((long long)p.slots * Hkv)));
+  if ((long long)p.slots * Hkv * a.S >= (1LL << 31) / (16 * p.nt)) return DQG_ERR_UNSUPPORTED;
+  return dqg::launch_kv4_attention(a, D, format, stream) == hipSuccess ? DQG_OK : DQG_ERR_HIP;
 }
 
 int packed_dequant_f32(const uint8_t* w, const uint16_t* s, int K, int N, int group,

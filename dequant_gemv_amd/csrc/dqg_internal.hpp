@@ -122,4 +122,45 @@ int router_splits(int H);
 hipError_t launch_router(const uint16_t* x, int T, int H, const uint16_t* wr, int E, float* part,
                          float* logits, hipStream_t st);
 
+
+// ---- 4-bit key/value cache (dqg_kv4.hip) ----------------------------------------------------
+// Where a call's rows and pages lie.  Sequence b owns rows cu[b] .. cu[b + 1) and its row i
+// stands at position lens[b] - (cu[b + 1] - cu[b]) + i.
+struct Kv4Where {
+  const int32_t* cu;     // [B + 1]
+  const int32_t* lens;   // [B]
+  const int32_t* table;  // [B, max_pages] page of each stretch of 2^page_shift positions
+  uint8_t* cache;        // [num_pages][Hkv][K codes | K scales | V codes | V scales]
+  int* status;           // error word, may be null
+  int T, B, max_pages, num_pages, Hkv, page_shift, group_shift;
+  int64_t page_bytes;    // of one page (all heads)
+  int head_bytes;        // of one head of a page
+};
+struct Kv4RowsArgs {
+  Kv4Where w;
+  const uint16_t* k;     // write: rows in;  read: null
+  const uint16_t* v;
+  uint16_t* k_out;       // read: rows out;  write: null
+  uint16_t* v_out;
+  int64_t k_stride, v_stride;  // elements from one row to the next
+};
+struct Kv4AttnArgs {
+  Kv4Where w;
+  const uint16_t* q;
+  int64_t q_stride, out_stride;
+  uint16_t* out;
+  float* lse;            // [T, Hq] or null
+  float* part;           // split partials (S > 1)
+  int Hq, r;             // query heads, and query heads per kv head
+  float scale;
+  int window, sinks;
+  int n_slots, S, nt;    // row-tile slots, kv splits, 16-row tiles per workgroup
+};
+constexpr int KV4_STEP = 32;  // tokens of one step of a wavefront
+hipError_t launch_kv4_write(const Kv4RowsArgs& a, int D, int fmt, hipStream_t st);
+hipError_t launch_kv4_read(const Kv4RowsArgs& a, int D, int fmt, hipStream_t st);
+hipError_t launch_kv4_attention(const Kv4AttnArgs& a, int D, int fmt, hipStream_t st);
+// bytes of one workgroup's partial: 16 nt rows of D sums, a maximum and a sum
+constexpr size_t kv4_part_floats(int nt, int D) { return (size_t)16 * nt * (D + 2); }
+
 }  // namespace dqg

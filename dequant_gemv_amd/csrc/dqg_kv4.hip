@@ -1,0 +1,921 @@
+// Key/value cache held in 4 bits: quantising rows as they are written, reading them back, and
+// attention over the cache.
+//
+// A page holds 2^page_shift positions of one sequence; for each kv head in turn
+//   K codes  [page][D / 2]          byte i of a position: d = 2 i low nibble, 2 i + 1 high
+//   K scales [page][D / G] bf16
+//   V codes  [page / 8][D][4]       byte i of (block, d): position 2 i of the block low, 2 i + 1 high
+//   V scales [page / 8][D / G][8] bf16
+// Each operand is packed along the axis its product sums over, as the packed weights are: scores
+// sum over d, outputs over positions.  A lane's operand of a 16x16x32 matrix instruction is 8
+// values along that axis, so one dword of codes decodes in place to one operand and no value
+// changes lanes.
+#include <float.h>
+#include <math.h>
+
+#include "dqg_device.hpp"
+#include "dqg_internal.hpp"
+
+namespace dqg {
+namespace {
+
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+constexpr int ST_PAGE = 1;    // status bit 0: a page id outside [0, num_pages)
+constexpr int ST_LENGTH = 2;  // status bit 1: a length beyond the table's positions
+
+__device__ __forceinline__ void report(int* status, int bit) {
+  if (status) atomicOr(status, bit);
+}
+
+// The sequence that slot `slot` falls to when sequence b's slots start at first(cu[b]) + b * per:
+// the count of sequences that start at or before it, 64 a step.  Uniform over the wavefront.
+template <class F>
+__device__ __forceinline__ int seq_of_slot(const Kv4Where& w, int slot, int per, F first) {
+  const int lane = threadIdx.x & 63;
+  int n = 0;
+  for (int b0 = 0; b0 < w.B; b0 += 64) {
+    const int b = b0 + lane;
+    bool at = false;
+    if (b < w.B) at = first(min(max(w.cu[b], 0), w.T)) + b * per <= slot;
+    const int c = __popcll(__ballot(at));
+    n += c;
+    if (c < 64) break;
+  }
+  return max(__builtin_amdgcn_readfirstlane(n) - 1, 0);
+}
+
+struct Seq {
+  int row0, n;   // rows row0 .. row0 + n - 1
+  int len, cap;  // positions, and how many of them the table has room for
+};
+__device__ __forceinline__ Seq seq_at(const Kv4Where& w, int b) {
+  Seq s;
+  s.row0 = min(max(w.cu[b], 0), w.T);
+  s.n = min(max(w.cu[b + 1], s.row0), w.T) - s.row0;
+  s.len = min(max(w.lens[b], 0), 0x7FFF0000);
+  s.cap = w.max_pages << w.page_shift;
+  return s;
+}
+
+__device__ __forceinline__ uint32_t pk_max_u16(uint32_t a, uint32_t b) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  const u16x2 x = __builtin_bit_cast(u16x2, a), y = __builtin_bit_cast(u16x2, b);
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(x, y));
+}
+
+// ---- quantisation -----------------------------------------------------------------------
+// s = bf16(amax / c), code = nearest(x / s).  x and s have 8 significant bits, so a quotient that
+// is no tie is at least 1 / 1020 away from every tie of either grid; fma(x, 1 / s, 1536) rounds
+// the quotient to multiples of 2^-13 with an error (reciprocal and fma, below 2^-18) that
+// cannot carry it across one, and lands exactly on a tie where the true quotient is one.  The
+// codes are therefore those of an exact division.
+struct GroupScale {
+  uint16_t bits;  // bf16 scale
+  float inv;      // 1 / scale, or 0
+};
+template <int FMT>
+__device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits) {
+  GroupScale g;
+  if (amax_bits >= 0x7F80u) {  // a NaN or an infinity: the group reads back as NaN
+    g.bits = 0x7FC0u;
+    g.inv = 0.0f;
+  } else if (amax_bits < 0x0D80u) {  // below 2^-100
+    g.bits = 0;
+    g.inv = 0.0f;
+  } else {
+    const float a = __uint_as_float(amax_bits << 16);
+    // (a / c is at least 1 / 3584 of itself away from a rounding tie: the product rounds alike)
+    g.bits = f32_to_bf16(a * (FMT == FMT_INT4 ? 1.0f / 7.0f : 1.0f / 6.0f));
+    g.inv = __builtin_amdgcn_rcpf(__uint_as_float((uint32_t)g.bits << 16));
+  }
+  return g;
+}
+// the code of x in the low 4 bits (INT4; the others hold rubbish)
+__device__ __forceinline__ uint32_t int4_code(float x, float inv) {
+  // 12582912 = 1.5 * 2^23: the sum's low bits are the rounded quotient (ties to even) + 8
+  return __float_as_uint(fmaf(x, inv, 1536.0f) + (12582912.0f + 8.0f - 1536.0f));
+}
+// (with the sign of x where it is zero: FP4 codes keep the sign)
+__device__ __forceinline__ float snapped(float x, float inv) {
+  return copysignf(fmaf(x, inv, 1536.0f) - 1536.0f, x);
+}
+// codes of 8 values, first in the low nibble
+template <int FMT>
+__device__ __forceinline__ uint32_t encode8(const float (&x)[8], const float (&inv)[8]) {
+  uint32_t w = 0;
+  if constexpr (FMT == FMT_INT4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w |= (int4_code(x[i], inv[i]) & 15u) << (4 * i);
+  } else {
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, snapped(x[0], inv[0]), snapped(x[1], inv[1]), 1.0f, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, snapped(x[2], inv[2]), snapped(x[3], inv[3]), 1.0f, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, snapped(x[4], inv[4]), snapped(x[5], inv[5]), 1.0f, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, snapped(x[6], inv[6]), snapped(x[7], inv[7]), 1.0f, 3);
+  }
+  return w;
+}
+template <int FMT>
+__device__ __forceinline__ void decode8(uint32_t w, float (&x)[8]) {
+  if constexpr (FMT == FMT_INT4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] = __uint_as_float(((w >> (4 * i)) & 15u) | 0x4B000000u) - 8388616.0f;
+  } else {
+    const f32x2_t a = fp4_pair_f32<0>(w), b = fp4_pair_f32<1>(w);
+    const f32x2_t c = fp4_pair_f32<2>(w), d = fp4_pair_f32<3>(w);
+    x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
+    x[4] = c.x; x[5] = c.y; x[6] = d.x; x[7] = d.y;
+  }
+}
+
+// Rows of one block of 8 aligned positions that the call writes or reads.  Rows before position
+// 0 (idle slots of a padded batch hold no position) lie in blocks of negative positions.
+struct Block {
+  int head, slot;  // slot: first position of the block within its page
+  int lo, hi;      // the call's rows are positions lo .. hi - 1 of the block
+  int64_t row;     // row of the block's first position (may be before the sequence's rows)
+  uint8_t* base;   // the head's part of the page
+  bool held;       // the block has a place in the cache
+};
+// Slots of a sequence: n rows touch at most floor((n + 14) / 8) blocks, and
+// floor(cu[b + 1] / 8) - floor(cu[b] / 8) + 2 >= ceil((n + 9) / 8) is at least that.
+__device__ __forceinline__ bool block_at(const Kv4Where& w, int slot, int head, Block& o) {
+  const int b = seq_of_slot(w, slot, 2, [](int c) { return c >> 3; });
+  const Seq s = seq_at(w, b);
+  const int first = s.len - s.n;  // position of row 0
+  const int pos0 = (first & ~7) + 8 * (slot - ((s.row0 >> 3) + 2 * b));
+  if (s.n <= 0 || pos0 >= s.len || pos0 + 8 <= first) return false;
+  o.head = head;
+  o.lo = max(first - pos0, 0);
+  o.hi = min(s.len - pos0, 8);
+  o.row = (int64_t)s.row0 + (pos0 - first);
+  o.slot = pos0 & ((1 << w.page_shift) - 1);
+  o.base = w.cache;
+  o.held = false;
+  if (pos0 < 0) return true;
+  int bad = ST_LENGTH;
+  if (pos0 < s.cap) {
+    const int page = w.table[(int64_t)b * w.max_pages + (pos0 >> w.page_shift)];
+    bad = ST_PAGE;
+    if (page >= 0 && page < w.num_pages) {
+      o.base += page * w.page_bytes + (int64_t)head * w.head_bytes;
+      o.held = true;
+    }
+  }
+  if (!o.held && (threadIdx.x & 63) == 0) report(w.status, bad);
+  return true;
+}
+
+// Byte offsets inside a head's part of a page.
+template <int D>
+struct Layout {
+  int n_shift;  // log2(D / G)
+  int ks, vc, vs;
+  __device__ __forceinline__ Layout(const Kv4Where& w) {
+    constexpr int lg = D == 64 ? 6 : D == 128 ? 7 : 8;
+    n_shift = lg - w.group_shift;
+    const int codes = (D / 2) << w.page_shift, scales = 2 << (w.page_shift + n_shift);
+    ks = codes;
+    vc = codes + scales;
+    vs = 2 * codes + scales;
+  }
+};
+
+// ---- write --------------------------------------------------------------------------------
+// K: 16 values of one position a lane (32-byte loads, 8-byte stores).  V: 2 columns of all 8
+// positions a lane, so that the lane owns whole dwords of codes; a block that the call does not
+// fill keeps the other positions' nibbles.
+template <int D, int FMT>
+__global__ __launch_bounds__(256) void kv4_write_kernel(Kv4RowsArgs a, int n_units) {
+  const int unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (unit >= n_units) return;
+  const int lane = threadIdx.x & 63;
+  const bool is_v = unit & 1;
+  const int hs = unit >> 1;
+  Block o;
+  if (!block_at(a.w, hs / a.w.Hkv, hs % a.w.Hkv, o) || !o.held) return;
+  const Layout<D> L(a.w);
+  const int gs = a.w.group_shift;
+  if (!is_v) {
+    constexpr int LT = D / 16;  // lanes a position
+#pragma unroll
+    for (int it = 0; it < (8 * LT + 63) / 64; ++it) {
+      const int item = it * 64 + lane, t = item / LT, d0 = (item % LT) * 16;
+      const bool on = t >= o.lo && t < o.hi;
+      uint4 x[2] = {};
+      if (on) {
+        const uint4* p = reinterpret_cast<const uint4*>(a.k + (o.row + t) * a.k_stride +
+                                                        (int64_t)o.head * D + d0);
+        x[0] = p[0];
+        x[1] = p[1];
+      }
+      const uint32_t u[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = pk_max_u16(m, u[i] & 0x7FFF7FFFu);
+      uint32_t am = max(m & 0xFFFFu, m >> 16);
+      am = max(am, (uint32_t)__shfl_xor((int)am, 1));
+      if (gs == 7) {
+        am = max(am, (uint32_t)__shfl_xor((int)am, 2));
+        am = max(am, (uint32_t)__shfl_xor((int)am, 4));
+      }
+      const GroupScale g = group_scale<FMT>(am);
+      uint32_t c[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float f[8], inv[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[2 * i] = bf16_lo(u[4 * h + i]);
+          f[2 * i + 1] = bf16_hi(u[4 * h + i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) inv[i] = g.inv;
+        c[h] = encode8<FMT>(f, inv);
+      }
+      if (on) {
+        *reinterpret_cast<uint2*>(o.base + (o.slot + t) * (D / 2) + d0 / 2) = make_uint2(c[0], c[1]);
+        if ((d0 & ((1 << gs) - 1)) == 0)
+          *reinterpret_cast<uint16_t*>(o.base + L.ks +
+                                       2 * (((o.slot + t) << L.n_shift) + (d0 >> gs))) = g.bits;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int it = 0; it < (D + 127) / 128; ++it) {
+      const int d0 = it * 128 + 2 * lane;
+      const bool mine = d0 < D;
+      uint32_t u[8];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        u[t] = 0;
+        if (mine && t >= o.lo && t < o.hi)
+          u[t] = *reinterpret_cast<const uint32_t*>(a.v + (o.row + t) * a.v_stride +
+                                                    (int64_t)o.head * D + d0);
+      }
+      float inv[8];
+      uint16_t bits[8];
+#pragma unroll
+      for (int t = 0; t < 8; t += 2) {  // two positions' maxima in one dword
+        const uint32_t x = u[t] & 0x7FFF7FFFu, y = u[t + 1] & 0x7FFF7FFFu;
+        uint32_t m = max(x & 0xFFFFu, x >> 16) | (max(y & 0xFFFFu, y >> 16) << 16);
+#pragma unroll
+        for (int k = 1; k < 16; k *= 2) m = pk_max_u16(m, (uint32_t)__shfl_xor((int)m, k));
+        if (gs == 7) {
+          m = pk_max_u16(m, (uint32_t)__shfl_xor((int)m, 16));
+          m = pk_max_u16(m, (uint32_t)__shfl_xor((int)m, 32));
+        }
+        const GroupScale g0 = group_scale<FMT>(m & 0xFFFFu), g1 = group_scale<FMT>(m >> 16);
+        inv[t] = g0.inv; bits[t] = g0.bits;
+        inv[t + 1] = g1.inv; bits[t + 1] = g1.bits;
+      }
+      float f0[8], f1[8];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        f0[t] = bf16_lo(u[t]);
+        f1[t] = bf16_hi(u[t]);
+      }
+      uint2 c = make_uint2(encode8<FMT>(f0, inv), encode8<FMT>(f1, inv));
+      if (mine) {
+        uint2* p = reinterpret_cast<uint2*>(o.base + L.vc + ((o.slot >> 3) * D + d0) * 4);
+        const bool whole = o.lo == 0 && o.hi == 8;
+        if (!whole) {
+          const uint32_t keep = ~(uint32_t)((((uint64_t)1 << (4 * o.hi)) - 1) &
+                                            ~(((uint64_t)1 << (4 * o.lo)) - 1));
+          const uint2 old = *p;
+          c.x = (c.x & ~keep) | (old.x & keep);
+          c.y = (c.y & ~keep) | (old.y & keep);
+        }
+        *p = c;
+        if ((d0 & ((1 << gs) - 1)) == 0) {
+          uint16_t* s = reinterpret_cast<uint16_t*>(
+              o.base + L.vs + 16 * (((o.slot >> 3) << L.n_shift) + (d0 >> gs)));
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+            if (t >= o.lo && t < o.hi) s[t] = bits[t];
+        }
+      }
+    }
+  }
+}
+
+// ---- read ---------------------------------------------------------------------------------
+// The same lanes the other way round.  Rows without a place in the cache (before position 0, or
+// behind the table, or in a page that is not there) read as zeros.
+template <int D, int FMT>
+__global__ __launch_bounds__(256) void kv4_read_kernel(Kv4RowsArgs a, int n_units) {
+  const int unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (unit >= n_units) return;
+  const int lane = threadIdx.x & 63;
+  const bool is_v = unit & 1;
+  const int hs = unit >> 1;
+  Block o;
+  if (!block_at(a.w, hs / a.w.Hkv, hs % a.w.Hkv, o)) return;
+  const Layout<D> L(a.w);
+  const int gs = a.w.group_shift;
+  if (!is_v) {
+    constexpr int LT = D / 16;
+#pragma unroll
+    for (int it = 0; it < (8 * LT + 63) / 64; ++it) {
+      const int item = it * 64 + lane, t = item / LT, d0 = (item % LT) * 16;
+      if (t < o.lo || t >= o.hi) continue;
+      uint2 c = make_uint2(0, 0);
+      float s = 0.0f;
+      if (o.held) {
+        c = *reinterpret_cast<const uint2*>(o.base + (o.slot + t) * (D / 2) + d0 / 2);
+        s = bf16_to_f32(*reinterpret_cast<const uint16_t*>(
+            o.base + L.ks + 2 * (((o.slot + t) << L.n_shift) + (d0 >> gs))));
+      }
+      float f[16];
+      {
+        float x[8], y[8];
+        decode8<FMT>(c.x, x);
+        decode8<FMT>(c.y, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          f[i] = o.held ? x[i] * s : 0.0f;
+          f[8 + i] = o.held ? y[i] * s : 0.0f;
+        }
+      }
+      uint32_t r[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bf16x2_t h = {(__bf16)f[2 * i], (__bf16)f[2 * i + 1]};
+        r[i] = __builtin_bit_cast(uint32_t, h);
+      }
+      uint4* p = reinterpret_cast<uint4*>(a.k_out + (o.row + t) * a.k_stride +
+                                          (int64_t)o.head * D + d0);
+      p[0] = make_uint4(r[0], r[1], r[2], r[3]);
+      p[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    }
+  } else {
+#pragma unroll
+    for (int it = 0; it < (D + 127) / 128; ++it) {
+      const int d0 = it * 128 + 2 * lane;
+      if (d0 >= D) continue;
+      uint2 c = make_uint2(0, 0);
+      uint4 sv = make_uint4(0, 0, 0, 0);
+      if (o.held) {
+        c = *reinterpret_cast<const uint2*>(o.base + L.vc + ((o.slot >> 3) * D + d0) * 4);
+        sv = *reinterpret_cast<const uint4*>(
+            o.base + L.vs + 16 * (((o.slot >> 3) << L.n_shift) + (d0 >> gs)));
+      }
+      const uint32_t sw[4] = {sv.x, sv.y, sv.z, sv.w};
+      float x[8], y[8];
+      decode8<FMT>(c.x, x);
+      decode8<FMT>(c.y, y);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        if (t < o.lo || t >= o.hi) continue;
+        const float s = (t & 1) ? bf16_hi(sw[t / 2]) : bf16_lo(sw[t / 2]);
+        const bf16x2_t h = {(__bf16)(o.held ? x[t] * s : 0.0f),
+                            (__bf16)(o.held ? y[t] * s : 0.0f)};
+        *reinterpret_cast<uint32_t*>(a.v_out + (o.row + t) * a.v_stride + (int64_t)o.head * D + d0) =
+            __builtin_bit_cast(uint32_t, h);
+      }
+    }
+  }
+}
+
+// ---- attention ----------------------------------------------------------------------------
+// Rows of a tile: row rho of sequence b is (query row rho / r, query head head * r + rho % r) of
+// one kv head, so the heads that share keys share a tile.  A wavefront takes 32 positions a step:
+//   S^T = K Q^T: A = K (16 positions x 32 d, decoded in place), B = Q^T.  The first matrix holds
+//     positions 8 g + 0..3, the second 8 g + 4..7 (g = 0..3), so that lane (q, g) ends up with
+//     positions 8 g .. 8 g + 7 of query row q;
+//   O^T += V^T P^T: A = V^T (one dword = 8 positions of one d), B = P^T: exactly the 8 values
+//     that the lane has.  Nothing passes through LDS or changes lanes.
+// Column j of d-tile (c, jj) of V^T is d = 64 c + 4 j + jj: a lane loads 4 d (16 bytes) at once.
+//
+// Operands are fp16: code value (<= 3 significant bits) times bf16 scale (8) is exact in fp16's
+// 11, where bf16 would round it; P enters scaled by 2^P_SHIFT against the running reference, so
+// that values down to 2^-18 of the largest keep 11 bits.  Sums, maxima and exponents are fp32.
+//
+// The reference maximum m moves only when a score passes it by more than MOVE (in powers of 2):
+// the steps in between need no exchange between lanes and no rescaling.  P stays below
+// 2^(P_SHIFT + MOVE) = 4096, well inside fp16.
+constexpr float MOVE = 8.0f;
+constexpr float P_SHIFT = 4.0f;
+
+struct Tile {
+  Seq s;
+  int b, head, rho0, n_rho;  // rows rho0 .. rho0 + n_rho - 1 of this (sequence, head)
+  int p_lo, p_hi;            // positions of the first and last row
+  int n_steps, sink_steps, main0;  // steps 0 .. sink_steps - 1, then main0, main0 + 1, ...
+};
+__device__ __forceinline__ bool tile_at(const Kv4AttnArgs& a, int slot, int head, int R, Tile& t) {
+  const Kv4Where& w = a.w;
+  const int r = a.r;
+  t.b = seq_of_slot(w, slot, 1, [=](int c) { return (int)((int64_t)c * r / R); });
+  t.s = seq_at(w, t.b);
+  const int j = slot - ((int)((int64_t)t.s.row0 * r / R) + t.b);
+  t.head = head;
+  t.rho0 = j * R;
+  t.n_rho = min(R, t.s.n * r - t.rho0);
+  if (j < 0 || t.n_rho <= 0) return false;
+  const int first = t.s.len - t.s.n;
+  t.p_lo = first + t.rho0 / r;
+  t.p_hi = first + (t.rho0 + t.n_rho - 1) / r;
+  const int end = min(t.p_hi + 1, t.s.cap);  // positions beyond the table hold nothing
+  t.n_steps = t.sink_steps = t.main0 = 0;
+  if (end > 0) {
+    const int last = (end - 1) / KV4_STEP;
+    if (a.window > 0 && t.p_lo >= a.window) {
+      t.main0 = (t.p_lo - a.window + 1) / KV4_STEP;
+      t.sink_steps = min((min(a.sinks, end) + KV4_STEP - 1) / KV4_STEP, min(t.main0, last + 1));
+    }
+    t.n_steps = t.sink_steps + max(last + 1 - t.main0, 0);
+  }
+  return true;
+}
+
+template <int D>
+struct Stage {  // one step's codes and scales of one lane
+  uint32_t kc[2][D / 32];
+  uint16_t ks[2][(D + 127) / 128];
+  uint32_t vc[D / 16];
+  uint4 vs[D / 64];
+  int t0;    // first position
+  bool ok;   // the page exists
+};
+
+template <int D>
+struct Offsets {  // per lane, inside a head's part of a page, for position 0
+  int kc[2], vc, ks[2][(D + 127) / 128], vs[D / 64];
+  __device__ __forceinline__ Offsets(const Kv4Where& w, int lane) {
+    const Layout<D> L(w);
+    const int m = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int row = 8 * (m >> 2) + (m & 3) + 4 * h;
+      kc[h] = row * (D / 2) + g * (D == 64 ? 8 : 16);
+#pragma unroll
+      for (int c = 0; c < (D + 127) / 128; ++c)
+        ks[h][c] = L.ks + 2 * ((row << L.n_shift) +
+                               ((128 * c + g * (D == 64 ? 16 : 32)) >> w.group_shift));
+    }
+    vc = L.vc + (g * D + 4 * m) * 4;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c)
+      vs[c] = L.vs + 16 * ((g << L.n_shift) + ((64 * c + 4 * m) >> w.group_shift));
+  }
+};
+
+template <int D>
+__device__ __forceinline__ void load_stage(const Kv4AttnArgs& a, const Tile& t, int step,
+                                           const Offsets<D>& off, Stage<D>& x) {
+  const Kv4Where& w = a.w;
+  const int j = step < t.sink_steps ? step : step - t.sink_steps + t.main0;
+  x.t0 = j * KV4_STEP;
+  const int page = __builtin_amdgcn_readfirstlane(
+      w.table[(int64_t)t.b * w.max_pages + (x.t0 >> w.page_shift)]);
+  x.ok = page >= 0 && page < w.num_pages;
+  const int in_page = x.t0 & ((1 << w.page_shift) - 1);
+  const int n_shift = (D == 64 ? 6 : D == 128 ? 7 : 8) - w.group_shift;
+  const uint8_t* base = w.cache + (x.ok ? page : 0) * w.page_bytes + (int64_t)t.head * w.head_bytes;
+  const uint8_t* codes = base + in_page * (D / 2);
+  const uint8_t* scales = base + ((in_page << n_shift) << 1);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if constexpr (D == 64) {
+      const uint2 c = *reinterpret_cast<const uint2*>(codes + off.kc[h]);
+      x.kc[h][0] = c.x;
+      x.kc[h][1] = c.y;
+    } else {
+#pragma unroll
+      for (int c = 0; c < D / 128; ++c) {
+        const uint4 u = *reinterpret_cast<const uint4*>(codes + off.kc[h] + 64 * c);
+        x.kc[h][4 * c] = u.x; x.kc[h][4 * c + 1] = u.y;
+        x.kc[h][4 * c + 2] = u.z; x.kc[h][4 * c + 3] = u.w;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < (D + 127) / 128; ++c)
+      x.ks[h][c] = *reinterpret_cast<const uint16_t*>(scales + off.ks[h][c]);
+  }
+#pragma unroll
+  for (int c = 0; c < D / 64; ++c) {
+    const uint4 u = *reinterpret_cast<const uint4*>(codes + off.vc + 256 * c);
+    x.vc[4 * c] = u.x; x.vc[4 * c + 1] = u.y; x.vc[4 * c + 2] = u.z; x.vc[4 * c + 3] = u.w;
+    x.vs[c] = *reinterpret_cast<const uint4*>(scales + off.vs[c]);
+  }
+}
+
+// Dword of 8 codes -> 8 fp16 values times the scales.  INT4: a nibble moved to mantissa bits
+// 6 .. 9 under the exponent of 16 reads as 16 + n; (16 + n) s - 24 s is one fma, exact because
+// 24 s is (3 more bits than s).  It leaves the pairs (0, 4), (1, 5), (2, 6), (3, 7): Q, P and the V
+// scales are laid out in that order.  FP4: the hardware's conversion, pairs (0, 1) .. (6, 7).
+template <int FMT>
+__device__ __forceinline__ f16x8_t decode_f16(uint32_t w, const f16x2_t (&s)[4],
+                                              const f16x2_t (&s24)[4]) {
+  f16x2_t p[4];
+  if constexpr (FMT == FMT_INT4) {
+    const uint32_t u[4] = {w << 6, w << 2, w >> 2, w >> 6};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      p[i] = __builtin_elementwise_fma(
+          __builtin_bit_cast(f16x2_t, (u[i] & 0x03C003C0u) | 0x4C004C00u), s[i], s24[i]);
+  } else {
+    p[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0) * s[0];
+    p[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1) * s[1];
+    p[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2) * s[2];
+    p[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3) * s[3];
+  }
+  struct { f16x2_t p[4]; } r = {{p[0], p[1], p[2], p[3]}};
+  return __builtin_bit_cast(f16x8_t, r);
+}
+// index of the value that operand half i holds
+template <int FMT>
+__host__ __device__ constexpr int value_at(int i) {
+  return FMT == FMT_INT4 ? (i >> 1) + 4 * (i & 1) : i;
+}
+
+template <int D, int FMT, int NT>
+struct Acc {
+  f32x4_t o[NT][D / 64][4];
+  float m[NT], l[NT];
+};
+
+template <int D, int FMT, int NT>
+__device__ __forceinline__ void attn_step(const Kv4AttnArgs& a, const Tile& t, const Stage<D>& x,
+                                          const f16x8_t (&q)[NT][D / 32], const int (&pos)[NT],
+                                          float c, int g, Acc<D, FMT, NT>& acc) {
+  if (!x.ok) return;
+  f32x4_t sc[NT][2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) sc[nt][h] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const _Float16 s1 = (_Float16)bf16_to_f32(x.ks[h][D == 64 ? 0 : i / 4]);
+      const f16x2_t s = {s1, s1};
+      const f16x2_t s24 = s * (f16x2_t){(_Float16)-24.0f, (_Float16)-24.0f};
+      const f16x2_t s4[4] = {s, s, s, s}, z4[4] = {s24, s24, s24, s24};
+      const f16x8_t k = decode_f16<FMT>(x.kc[h][i], s4, z4);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        sc[nt][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[nt][i], sc[nt][h], 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)  // scores in powers of 2
+#pragma unroll
+    for (int h = 0; h < 2; ++h) sc[nt][h] *= c;
+  // V scales of the lane's 8 positions, two groups' worth at most per 64 columns
+  f16x2_t vs[D / 64][4], vs24[D / 64][4];
+  uint32_t vw[D / 64][4];
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e) {
+    vw[e][0] = x.vs[e].x; vw[e][1] = x.vs[e].y; vw[e][2] = x.vs[e].z; vw[e][3] = x.vs[e].w;
+  }
+  const bool edge = x.t0 + KV4_STEP - 1 > t.p_lo ||
+                    (a.window > 0 && x.t0 <= t.p_hi - a.window && x.t0 + KV4_STEP > a.sinks);
+  if (edge) {
+    // hidden positions may hold anything: their scores are replaced and their V scales cleared.
+    // A position with a non-finite V scale that only some rows see is cleared too, and the rows
+    // that see it get a NaN score.
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int p = x.t0 + 8 * g + i;
+      bool bad = false;
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e) {
+        const uint32_t b16 = (i & 1) ? vw[e][i / 2] >> 16 : vw[e][i / 2] & 0xFFFFu;
+        bad |= (b16 & 0x7F80u) == 0x7F80u;
+      }
+      const uint64_t bads = __ballot(bad);
+      const bool poisoned = ((bads >> (16 * g)) & 0xFFFFu) != 0;
+      if (poisoned || p > t.p_hi)
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e)
+          vw[e][i / 2] &= (i & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const bool seen = p <= pos[nt] &&
+                          (a.window == 0 || p > pos[nt] - a.window || p < a.sinks);
+        const float s = sc[nt][i >> 2][i & 3];
+        sc[nt][i >> 2][i & 3] = !seen ? -INFINITY : poisoned ? NAN : s;
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int i0 = value_at<FMT>(2 * i), i1 = value_at<FMT>(2 * i + 1);
+      const float s0 = (i0 & 1) ? bf16_hi(vw[e][i0 / 2]) : bf16_lo(vw[e][i0 / 2]);
+      const float s1 = (i1 & 1) ? bf16_hi(vw[e][i1 / 2]) : bf16_lo(vw[e][i1 / 2]);
+      vs[e][i] = f16x2_t{(_Float16)s0, (_Float16)s1};
+      vs24[e][i] = vs[e][i] * (f16x2_t){(_Float16)-24.0f, (_Float16)-24.0f};
+    }
+  // the reference moves where one passes it by more than MOVE
+  bool move = false;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, sc[nt][i >> 2][i & 3]);
+    move |= mx > acc.m[nt] + MOVE;
+  }
+  if (__ballot(move)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float mx = acc.m[nt];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mx = fmaxf(mx, sc[nt][i >> 2][i & 3]);
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      const float f = __builtin_amdgcn_exp2f(acc.m[nt] - mx);
+      acc.m[nt] = mx;
+      acc.l[nt] *= f;
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e)
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) acc.o[nt][e][jj] *= f;
+    }
+  }
+  f16x8_t p[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float v[8], sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = __builtin_amdgcn_exp2f(sc[nt][i >> 2][i & 3] - (acc.m[nt] - P_SHIFT));
+      sum += v[i];
+    }
+    acc.l[nt] += sum;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[nt][i] = (_Float16)v[value_at<FMT>(i)];
+  }
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e)
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) {
+      const f16x8_t v = decode_f16<FMT>(x.vc[4 * e + jj], vs[e], vs24[e]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        acc.o[nt][e][jj] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[nt], acc.o[nt][e][jj], 0, 0, 0);
+    }
+}
+
+// Splits of a tile: `per` steps each, the last shorter.
+__device__ __forceinline__ int steps_per_split(int n_steps, int S) {
+  return max((n_steps + S - 1) / S, 1);
+}
+
+// One row of the result: o = sum / l (zero where nothing was visible), lse = ln(sum of exp).
+__device__ __forceinline__ float row_lse(float m, float l) {
+  return l > 0.0f || l != l ? (m - P_SHIFT) * LN2 + logf(l) : -INFINITY;
+}
+
+// One workgroup per (row tile, kv split, kv head); its 4 wavefronts take the split's steps in
+// turn and join their sums through LDS in a fixed order.
+template <int D, int FMT, int NT>
+__global__ __launch_bounds__(256) void kv4_attn_kernel(Kv4AttnArgs a) {
+  constexpr int R = 16 * NT, LD = D + 4;
+  __shared__ float lds_o[3][16][LD];
+  __shared__ float lds_m[4][R], lds_l[4][R];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q16 = lane & 15, g = lane >> 4;
+  const int head = blockIdx.x % a.w.Hkv, rest = blockIdx.x / a.w.Hkv;
+  const int split = rest % a.S, slot = a.n_slots - 1 - rest / a.S;
+  Tile t;
+  if (!tile_at(a, slot, head, R, t)) return;
+  if (t.s.len > t.s.cap && split == 0 && threadIdx.x == 0) report(a.w.status, ST_LENGTH);
+  const int per = steps_per_split(t.n_steps, a.S);
+  const int s0 = split * per, s1 = min(s0 + per, t.n_steps);
+  if (split > 0 && s0 >= t.n_steps) return;
+
+  // Q^T operands: lane (q, g) holds the d of K dword i of chunk i / 4 in that dword's value order
+  f16x8_t q[NT][D / 32];
+  int pos[NT];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int rho = t.rho0 + 16 * nt + q16;
+    const bool on = 16 * nt + q16 < t.n_rho;
+    const int i = rho / a.r, h = t.head * a.r + rho % a.r;
+    pos[nt] = on ? t.s.len - t.s.n + i : -1;
+    const uint16_t* p = a.q + (int64_t)(t.s.row0 + i) * a.q_stride + (int64_t)h * D;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      const int d0 = D == 64 ? 16 * g + 8 * j : 128 * (j / 4) + 32 * g + 8 * (j % 4);
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (on) u = *reinterpret_cast<const uint4*>(p + d0);
+      const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int d = value_at<FMT>(e);
+        q[nt][j][e] = (_Float16)((d & 1) ? bf16_hi(uw[d / 2]) : bf16_lo(uw[d / 2]));
+      }
+    }
+  }
+  Acc<D, FMT, NT> acc;
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    acc.m[nt] = -FLT_MAX;
+    acc.l[nt] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e)
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) acc.o[nt][e][jj] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  const float c = a.scale * LOG2E;
+  const Offsets<D> off(a.w, lane);
+  bool all_ok = true;
+  int step = s0 + wave;
+  if (step < s1) {
+    Stage<D> x, y;
+    load_stage<D>(a, t, step, off, x);
+    while (true) {
+      const bool more = step + 4 < s1;
+      if (more) load_stage<D>(a, t, step + 4, off, y);
+      all_ok &= x.ok;
+      attn_step<D, FMT, NT>(a, t, x, q, pos, c, g, acc);
+      if (!more) break;
+      step += 4;
+      x = y;
+    }
+  }
+  if (!all_ok && lane == 0) report(a.w.status, ST_PAGE);
+
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    float l = acc.l[nt];
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (g == 0) {
+      lds_m[wave][16 * nt + q16] = acc.m[nt];
+      lds_l[wave][16 * nt + q16] = l;
+    }
+  }
+  __syncthreads();
+  const bool whole = per >= t.n_steps;  // this split is the tile's only one
+  float* part = whole ? nullptr
+                      : a.part + (((int64_t)slot * a.w.Hkv + head) * a.S + split) *
+                                     (int64_t)(R * (D + 2));
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int row = 16 * nt + q16;
+    float m = lds_m[0][row];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) m = fmaxf(m, lds_m[w][row]);
+    float l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) l += lds_l[w][row] * __builtin_amdgcn_exp2f(lds_m[w][row] - m);
+    const float f = __builtin_amdgcn_exp2f(acc.m[nt] - m);
+    if (nt > 0) __syncthreads();
+    // wavefront nt collects: the others leave their sums in LDS, lower wavefronts first
+    if (wave != nt) {
+      float* dst = &lds_o[wave < nt ? wave : wave - 1][q16][0];
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4*>(dst + 64 * e + 16 * g + 4 * i) =
+              make_float4(acc.o[nt][e][0][i] * f, acc.o[nt][e][1][i] * f, acc.o[nt][e][2][i] * f,
+                          acc.o[nt][e][3][i] * f);
+    }
+    __syncthreads();
+    if (wave == nt && row < t.n_rho) {
+      const int rho = t.rho0 + row, qi = t.s.row0 + rho / a.r, h = t.head * a.r + rho % a.r;
+      const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+      uint16_t* out = a.out + (int64_t)qi * a.out_stride + (int64_t)h * D;
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e) {
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float4 u = make_float4(acc.o[nt][e][0][i] * f, acc.o[nt][e][1][i] * f,
+                                 acc.o[nt][e][2][i] * f, acc.o[nt][e][3][i] * f);
+#pragma unroll
+          for (int w = 0; w < 3; ++w) {
+            const float4 z = *reinterpret_cast<const float4*>(&lds_o[w][q16][64 * e + 16 * g + 4 * i]);
+            u.x += z.x; u.y += z.y; u.z += z.z; u.w += z.w;
+          }
+          v[4 * i] = u.x; v[4 * i + 1] = u.y; v[4 * i + 2] = u.z; v[4 * i + 3] = u.w;
+        }
+        if (whole) {
+          uint32_t b[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const bf16x2_t hh = {(__bf16)(v[2 * i] * inv), (__bf16)(v[2 * i + 1] * inv)};
+            b[i] = __builtin_bit_cast(uint32_t, hh);
+          }
+          uint4* dst = reinterpret_cast<uint4*>(out + 64 * e + 16 * g);
+          dst[0] = make_uint4(b[0], b[1], b[2], b[3]);
+          dst[1] = make_uint4(b[4], b[5], b[6], b[7]);
+        } else {
+          float4* dst = reinterpret_cast<float4*>(part + row * D + 64 * e + 16 * g);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        }
+      }
+      if (g == 0) {
+        if (!whole) {
+          part[R * D + row] = m;
+          part[R * D + R + row] = l;
+        } else if (a.lse) {
+          a.lse[(int64_t)qi * a.Hq + h] = row_lse(m, l);
+        }
+      }
+    }
+  }
+}
+
+// Joins the splits of a tile, ascending: one wavefront per row, D / 64 columns a lane.
+template <int D>
+__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs a, int R) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int groups = R / 4;  // 4 rows a workgroup
+  const int head = blockIdx.x % a.w.Hkv, rest = blockIdx.x / a.w.Hkv;
+  const int slot = rest / groups, row = 4 * (rest % groups) + wave;
+  Tile t;
+  if (!tile_at(a, slot, head, R, t) || row >= t.n_rho) return;
+  const int per = steps_per_split(t.n_steps, a.S);
+  const int n = (t.n_steps + per - 1) / per;
+  if (n <= 1) return;
+  const int64_t size = (int64_t)R * (D + 2);
+  const float* part = a.part + ((int64_t)slot * a.w.Hkv + head) * a.S * size;
+  float m = -FLT_MAX;
+  for (int s = 0; s < n; ++s) m = fmaxf(m, part[s * size + R * D + row]);
+  float l = 0.0f, o[D / 64];
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e) o[e] = 0.0f;
+  for (int s = 0; s < n; ++s) {
+    const float* p = part + s * size;
+    const float f = __builtin_amdgcn_exp2f(p[R * D + row] - m);
+    l += f * p[R * D + R + row];
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) o[e] += f * p[row * D + 64 * e + lane];
+  }
+  const int rho = t.rho0 + row, qi = t.s.row0 + rho / a.r, h = t.head * a.r + rho % a.r;
+  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  uint16_t* out = a.out + (int64_t)qi * a.out_stride + (int64_t)h * D;
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e)
+    out[64 * e + lane] = __builtin_bit_cast(uint16_t, (__bf16)(o[e] * inv));
+  if (a.lse && lane == 0) a.lse[(int64_t)qi * a.Hq + h] = row_lse(m, l);
+}
+
+template <int D, int FMT>
+hipError_t launch_rows(const Kv4RowsArgs& a, hipStream_t st) {
+  const int64_t units = 2 * (int64_t)a.w.Hkv * ((a.w.T >> 3) + 2 * (int64_t)a.w.B);
+  const dim3 grid((unsigned)((units + 3) / 4));
+  if (a.k)
+    kv4_write_kernel<D, FMT><<<grid, 256, 0, st>>>(a, (int)units);
+  else
+    kv4_read_kernel<D, FMT><<<grid, 256, 0, st>>>(a, (int)units);
+  return hipGetLastError();
+}
+
+template <int D, int FMT, int NT>
+hipError_t launch_attn(const Kv4AttnArgs& a, hipStream_t st) {
+  const unsigned tiles = (unsigned)a.n_slots * a.w.Hkv;
+  kv4_attn_kernel<D, FMT, NT><<<tiles * a.S, 256, 0, st>>>(a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.S == 1) return e;
+  kv4_join_kernel<D><<<tiles * (4 * NT), 256, 0, st>>>(a, 16 * NT);
+  return hipGetLastError();
+}
+template <int D, int FMT>
+hipError_t launch_attn(const Kv4AttnArgs& a, hipStream_t st) {
+  if (a.nt == 1) return launch_attn<D, FMT, 1>(a, st);
+  if (a.nt == 2 || D > 128) return launch_attn<D, FMT, 2>(a, st);
+  if constexpr (D <= 128) return launch_attn<D, FMT, 4>(a, st);
+  return hipErrorInvalidValue;
+}
+template <template <int, int> class L, class A>
+hipError_t by_type(const A& a, int D, int fmt, hipStream_t st) {
+  if (fmt == FMT_INT4)
+    return D == 64 ? L<64, FMT_INT4>::go(a, st)
+                   : D == 128 ? L<128, FMT_INT4>::go(a, st) : L<256, FMT_INT4>::go(a, st);
+  return D == 64 ? L<64, FMT_FP4>::go(a, st)
+                 : D == 128 ? L<128, FMT_FP4>::go(a, st) : L<256, FMT_FP4>::go(a, st);
+}
+template <int D, int FMT>
+struct Rows {
+  static hipError_t go(const Kv4RowsArgs& a, hipStream_t st) { return launch_rows<D, FMT>(a, st); }
+};
+template <int D, int FMT>
+struct Attn {
+  static hipError_t go(const Kv4AttnArgs& a, hipStream_t st) { return launch_attn<D, FMT>(a, st); }
+};
+
+}  // namespace
+
+hipError_t launch_kv4_write(const Kv4RowsArgs& a, int D, int fmt, hipStream_t st) {
+  return by_type<Rows>(a, D, fmt, st);
+}
+hipError_t launch_kv4_read(const Kv4RowsArgs& a, int D, int fmt, hipStream_t st) {
+  return by_type<Rows>(a, D, fmt, st);
+}
+hipError_t launch_kv4_attention(const Kv4AttnArgs& a, int D, int fmt, hipStream_t st) {
+  return by_type<Attn>(a, D, fmt, st);
+}
+
+}  // namespace dqg

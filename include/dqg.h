@@ -339,6 +339,101 @@ int packed_gemv_int4_tiled(const uint16_t* x, int T, int K, int N, const uint8_t
                            size_t workspace_bytes, hipStream_t stream);
 
 /*
+ * Key/value cache held in 4 bits (FireEcho page: "Flat KV cache" and the quantised KV cache of
+ * "Quantization Formats"; here with the library's own 4-bit formats), in pages.
+ *   cache       uint8 [num_pages, kv4_page_bytes].  A page holds page_size positions of one
+ *               sequence; for each of the Hkv kv heads in turn, G = group:
+ *                 K codes  [page_size][D / 2]       byte i of a position: d = 2 i in bits 0-3,
+ *                                                   2 i + 1 in bits 4-7
+ *                 K scales [page_size][D / G] bf16
+ *                 V codes  [page_size / 8][D][4]    byte i of (block, d): position 2 i of the
+ *                                                   block in bits 0-3, 2 i + 1 in bits 4-7
+ *                 V scales [page_size / 8][D / G][8] bf16
+ *               (each operand is packed along the axis that its product sums over, like the
+ *               packed weights).  A value is value(code) * scale with the element values of
+ *               DQG_FMT_INT4 or DQG_FMT_FP4_E2M1.
+ *   block_table int32 [B, max_pages]: position t of sequence b lies in page
+ *               block_table[b, t / page_size].  Entries behind a sequence's positions are not
+ *               looked up.
+ *   cu_rows     int32 [B + 1], ascending from 0: sequence b owns rows cu_rows[b] ..
+ *               cu_rows[b + 1] - 1 (n_b of them, none allowed) of the [T, ...] row tensors.
+ *               Rows from cu_rows[B] on belong to nobody: they are not read, and output rows
+ *               there are left as they were.
+ *   kv_lens     int32 [B]: positions of each sequence, the call's rows included; row i of
+ *               sequence b stands at position p = kv_lens[b] - n_b + i.  Rows before position 0
+ *               (a padded batch's idle slots: kv_lens[b] = 0) are not stored, read as zeros and
+ *               attend to nothing.
+ *   status      NULL, or a device int32 into which a call ORs bit 0 when it met a page id
+ *               outside [0, num_pages) (its positions are not stored, read as zeros, and are
+ *               invisible to attention) and bit 1 when kv_lens[b] > max_pages * page_size (the
+ *               positions beyond likewise).  The caller clears it.
+ * All of cu_rows, kv_lens and block_table are read on the device.  Limits: D in {64, 128, 256},
+ * G in {32, 128} dividing D, page_size a power of two from 32 to 65536, max_pages * page_size
+ * <= 2^30, B <= 65536, T <= 2^22, Hkv <= 1024.  cache and the row tensors 16-byte aligned, row
+ * strides (in elements) multiples of 8 and at least heads * D: rows may be columns of a wider
+ * matrix.  Two sequences that own rows of one kv4_write call must not share the pages that
+ * these rows fall into.
+ */
+
+/* Host only: bytes of one page, Hkv * page_size * (D + 4 D / G).  0 for unsupported sizes. */
+size_t kv4_page_bytes(int Hkv, int D, int page_size, int group);
+
+/*
+ * kv4_write -- quantises rows k and v (bf16 [T, Hkv, D]) into the cache.  Per row, head and group
+ * of G values x: a = max |x|; scale = bf16_rne(a / 7) (INT4) or bf16_rne(a / 6) (FP4), 0 where
+ * a < 2^-100, NaN where the group holds a NaN or an infinity (it reads back as NaN); code = the
+ * nearest of x / scale, ties to the even code (FP4: with the sign of x, also of zeros).  Exactly these codes on every call: the result
+ * does not depend on T or on the rows' grouping into calls.  Positions that the call does not
+ * write keep their values.
+ */
+int kv4_write(const uint16_t* k, const uint16_t* v, int T, int64_t k_stride, int64_t v_stride,
+              int B, const int32_t* cu_rows, const int32_t* kv_lens, const int32_t* block_table,
+              int max_pages, uint8_t* cache, int num_pages, int Hkv, int D, int page_size,
+              int group, int format, int* status, hipStream_t stream);
+
+/* kv4_read -- the rows' values back, bf16_rne(value(code) * scale), into k and v [T, Hkv, D]. */
+int kv4_read(uint16_t* k, uint16_t* v, int T, int64_t k_stride, int64_t v_stride, int B,
+             const int32_t* cu_rows, const int32_t* kv_lens, const int32_t* block_table,
+             int max_pages, const uint8_t* cache, int num_pages, int Hkv, int D, int page_size,
+             int group, int format, int* status, hipStream_t stream);
+
+/*
+ * Host only: bytes of workspace with which kv4_attention splits long caches over workgroups, for
+ * up to T rows of B sequences of up to max_kv_len positions (0: such calls never split).  0 also
+ * for invalid sizes.  Grows with T, B and max_kv_len.
+ */
+size_t kv4_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int max_kv_len);
+
+/*
+ * kv4_attention -- causal attention of rows q (bf16 [T, Hq, D]) over the cached keys and values,
+ * for prompts, chunks of prompts and single tokens alike (write the rows' own keys and values
+ * first).  Query head h reads kv head h / (Hq / Hkv).  For row i at position p:
+ *   S[t] = scale * sum_d q[i, d] K[t, d],
+ *   out[i] = bf16_rne( sum_t softmax(S)[t] V[t] ),  lse[i] = ln( sum_t exp(S[t]) )
+ * over the visible positions t: t <= p, and where window > 0 also t > p - window or t < sinks (the
+ * first `sinks` positions stay visible).  A row that sees nothing is 0, its lse -inf.  What
+ * hidden positions hold (NaN, infinite scales, old data) changes nothing; a visible NaN
+ * makes the row's components NaN, some or all.
+ *   lse      fp32 [T, Hq] or NULL
+ *   max_rows, max_kv_len: no sequence has more rows or positions than these (0: not known).
+ *            They choose the launch shape only; the result is right for any value.
+ *   workspace NULL (no splits: correct, slower where few rows meet a long cache), or at least
+ *            kv4_attention_workspace_bytes(T, B, Hq, Hkv, D, max_kv_len, or max_pages *
+ *            page_size where that is 0).  Scratch: no contents are expected or kept.
+ * Products on fp16 matrix cores with fp32 sums.  Cached values enter exactly for scales from
+ * 2^-17 on (below, within 2^-25 of the value per code step) and must stay below 16384 (INT4) or
+ * 65504 (FP4) in magnitude; |q| < 65504, and |q| < 2^-14 enters within 2^-25.  Softmax
+ * statistics in fp32.  Deterministic for equal arguments.
+ * scale finite.  Calls that may run at the same time must not share a workspace.
+ */
+int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32_t* cu_rows,
+                  const int32_t* kv_lens, const int32_t* block_table, int max_pages,
+                  const uint8_t* cache, int num_pages, int Hq, int Hkv, int D, int page_size,
+                  int group, int format, float scale, int window, int sinks, int max_rows,
+                  int max_kv_len, uint16_t* out, int64_t out_stride, float* lse, int* status,
+                  void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
  * packed_dequant_f32 -- TEST AID: dequantize one packed matrix with the same in-register
  * decode the compute kernels use.  w uint8 [K/2, N] (FP8: [K, N]), s bf16 [K/G, N] -> out
  * fp32 [K, N], out[k, n] = value(code[k, n]) * s[k/G, n], exact.
