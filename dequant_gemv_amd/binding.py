@@ -410,73 +410,81 @@ def kv4_cache(num_pages: int, kv_heads: int, head_dim: int, page_size: int, grou
     return torch.zeros((num_pages, n), dtype=torch.uint8, device=device)
 
 
-def _need_rows(t: torch.Tensor, name: str, T: int, heads: int, D: int, device):
-    """bf16 [T, heads, D] whose rows may be columns of a wider matrix: only the row stride is
-    free.  Returns it."""
+def _refuse(t, name: str, dtype, shape, dev: int):
+    """The error for a tensor that a check turned down."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
-        raise TypeError(f"{name} must be bf16 (or its 16-bit patterns), got {t.dtype}")
-    if t.shape != (T, heads, D):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, heads, D)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous (row tensors: heads and dims of a row)")
+
+
+def _need_rows(t: torch.Tensor, name: str, shape, dev: int):
+    """bf16 [T, heads, D] whose rows may be columns of a wider matrix: only the row stride is
+    free.  Returns it."""
+    if (not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.shape != shape
+            or t.get_device() != dev):
+        _refuse(t, name, torch.bfloat16, shape, dev)
+    T, heads, D = shape
     s0, s1, s2 = t.stride()
-    if s2 != 1 or (heads > 1 and s1 != D):
-        raise ValueError(f"{name}: heads and dims of a row must be contiguous")
+    if s2 != 1 or (s1 != D and heads > 1):
+        _refuse(t, name, torch.bfloat16, shape, dev)
     return s0 if T > 1 else max(s0, heads * D)
 
 
-def _need_i32(t: torch.Tensor, name: str, shape, device):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name} must be int32, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+def _need_flat(t: torch.Tensor, name: str, dtype, shape, dev: int):
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape
+            or t.get_device() != dev or not t.is_contiguous()):
+        _refuse(t, name, dtype, shape, dev)
 
 
 def _kv4_where(cu_rows, kv_lens, block_table, cache, kv_heads, D, page_size, group, status):
     """Checks what the cache calls share; returns (device, B, max_pages, num_pages)."""
-    if not isinstance(cache, torch.Tensor):
-        raise TypeError("cache must be a torch.Tensor")
-    dev = cache.device
-    if dev.type != "cuda":
+    if not isinstance(cache, torch.Tensor) or not isinstance(block_table, torch.Tensor):
+        raise TypeError("cache and block_table must be torch.Tensors")
+    if not cache.is_cuda:
         raise ValueError("cache must be a device tensor")
-    n = LIB.kv4_page_bytes(kv_heads, D, page_size, group)
-    if n == 0:
-        raise ValueError(f"unsupported cache sizes: {kv_heads} heads of {D}, pages of {page_size}, "
-                         f"group {group}")
-    if cache.dtype != torch.uint8 or cache.dim() != 2 or cache.shape[1] != n:
+    if group not in (32, 128):
+        raise ValueError(f"unsupported group {group}")
+    n = kv_heads * page_size * (D + 4 * D // group)  # kv4_page_bytes where the sizes are supported
+    if cache.dtype is not torch.uint8 or cache.dim() != 2 or cache.shape[1] != n:
         raise ValueError(f"cache must be uint8 [pages, {n}], got {cache.dtype} "
                          f"{tuple(cache.shape)}")
     if not cache.is_contiguous():
         raise ValueError("cache must be contiguous")
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise ValueError("block_table must be an int32 tensor [B, max_pages]")
-    B, max_pages = block_table.shape
-    _need_i32(block_table, "block_table", (B, max_pages), dev)
-    _need_i32(cu_rows, "cu_rows", (B + 1,), dev)
-    _need_i32(kv_lens, "kv_lens", (B,), dev)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [B, max_pages]")
+    dev = cache.get_device()
+    shape = block_table.shape
+    _need_flat(block_table, "block_table", torch.int32, shape, dev)
+    B = shape[0]
+    _need_flat(cu_rows, "cu_rows", torch.int32, (B + 1,), dev)
+    _need_flat(kv_lens, "kv_lens", torch.int32, (B,), dev)
     if status is not None:
-        _need_i32(status, "status", (1,), dev)
-    return dev, B, max_pages, cache.shape[0]
+        _need_flat(status, "status", torch.int32, (1,), dev)
+    return dev, B, shape[1], cache.shape[0]
 
 
-def _call(fn: str, device, *args):
-    """Calls an entry point on the device's current stream, with the device current."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        rc = getattr(LIB, fn)(*args, stream)
+def _call(name: str, fn, dev: int, *args):
+    """Calls an entry point on the device's current stream, with the device current (the null
+    stream belongs to the current device)."""
+    if torch.cuda.current_device() == dev:
+        rc = fn(*args, _raw_stream(dev))
     else:
-        with torch.cuda.device(device):
-            rc = getattr(LIB, fn)(*args, stream)
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev))
     if rc != DQG_OK:
-        raise DqgError(fn, rc)
+        raise DqgError(name, rc)
+
+
+# the stream's handle without a Stream object around it (1.9 us a call); the attribute is not a
+# public one, hence the way without it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _addr(t: Optional[torch.Tensor]):
@@ -493,9 +501,9 @@ def kv4_write(k, v, cu_rows, kv_lens, block_table, cache, page_size: int, group:
     T, H, D = k.shape
     dev, B, mp, pages = _kv4_where(cu_rows, kv_lens, block_table, cache, H, D, page_size, group,
                                    status)
-    ks = _need_rows(k, "k", T, H, D, dev)
-    vs = _need_rows(v, "v", T, H, D, dev)
-    _call("kv4_write", dev, k.data_ptr(), v.data_ptr(), T, ks, vs, B, cu_rows.data_ptr(),
+    ks = _need_rows(k, "k", k.shape, dev)
+    vs = _need_rows(v, "v", k.shape, dev)
+    _call("kv4_write", LIB.kv4_write, dev, k.data_ptr(), v.data_ptr(), T, ks, vs, B, cu_rows.data_ptr(),
           kv_lens.data_ptr(), block_table.data_ptr(), mp, cache.data_ptr(), pages, H, D, page_size,
           group, fmt, _addr(status))
 
@@ -507,13 +515,14 @@ def kv4_read(T: int, kv_heads: int, head_dim: int, cu_rows, kv_lens, block_table
     are allocated when not given; rows behind the last sequence are left as they are)."""
     dev, B, mp, pages = _kv4_where(cu_rows, kv_lens, block_table, cache, kv_heads, head_dim,
                                    page_size, group, status)
+    shape = (T, kv_heads, head_dim)
     if k is None:
-        k = torch.empty((T, kv_heads, head_dim), dtype=torch.bfloat16, device=dev)
+        k = cache.new_empty(shape, dtype=torch.bfloat16)
     if v is None:
-        v = torch.empty((T, kv_heads, head_dim), dtype=torch.bfloat16, device=dev)
-    ks = _need_rows(k, "k", T, kv_heads, head_dim, dev)
-    vs = _need_rows(v, "v", T, kv_heads, head_dim, dev)
-    _call("kv4_read", dev, k.data_ptr(), v.data_ptr(), T, ks, vs, B, cu_rows.data_ptr(),
+        v = cache.new_empty(shape, dtype=torch.bfloat16)
+    ks = _need_rows(k, "k", shape, dev)
+    vs = _need_rows(v, "v", shape, dev)
+    _call("kv4_read", LIB.kv4_read, dev, k.data_ptr(), v.data_ptr(), T, ks, vs, B, cu_rows.data_ptr(),
           kv_lens.data_ptr(), block_table.data_ptr(), mp, cache.data_ptr(), pages, kv_heads,
           head_dim, page_size, group, fmt, _addr(status))
     return k, v
@@ -526,9 +535,10 @@ def kv4_attention_workspace_bytes(T: int, B: int, heads: int, kv_heads: int, hea
 
 def kv4_workspace(T: int, B: int, heads: int, kv_heads: int, head_dim: int, max_kv_len: int,
                   device) -> Optional[torch.Tensor]:
-    """Scratch for kv4_attention calls of up to these sizes, or None where none is needed."""
+    """A workspace (zero-filled) for kv4_attention calls of up to these sizes, or None where none is
+    needed."""
     n = kv4_attention_workspace_bytes(T, B, heads, kv_heads, head_dim, max_kv_len)
-    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+    return torch.zeros(n, dtype=torch.uint8, device=device) if n else None
 
 
 def kv4_attention(q, cu_rows, kv_lens, block_table, cache, kv_heads: int, page_size: int,
@@ -545,17 +555,15 @@ def kv4_attention(q, cu_rows, kv_lens, block_table, cache, kv_heads: int, page_s
     T, H, D = q.shape
     dev, B, mp, pages = _kv4_where(cu_rows, kv_lens, block_table, cache, kv_heads, D, page_size,
                                    group, status)
-    qs = _need_rows(q, "q", T, H, D, dev)
+    qs = _need_rows(q, "q", q.shape, dev)
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
-    os_ = _need_rows(out, "out", T, H, D, dev)
+        out = cache.new_empty(q.shape, dtype=torch.bfloat16)
+    os_ = _need_rows(out, "out", q.shape, dev)
     if lse is not None:
-        if lse.dtype != torch.float32:
-            raise TypeError(f"lse must be float32, got {lse.dtype}")
-        _need(lse, "lse", 4, (T, H), dev)
+        _need_flat(lse, "lse", torch.float32, (T, H), dev)
     if workspace is not None:
-        _need(workspace, "workspace", 1, None, dev)
-    _call("kv4_attention", dev, q.data_ptr(), T, qs, B, cu_rows.data_ptr(), kv_lens.data_ptr(),
+        _need_flat(workspace, "workspace", torch.uint8, workspace.shape, dev)
+    _call("kv4_attention", LIB.kv4_attention, dev, q.data_ptr(), T, qs, B, cu_rows.data_ptr(), kv_lens.data_ptr(),
           block_table.data_ptr(), mp, cache.data_ptr(), pages, H, kv_heads, D, page_size, group,
           fmt, scale, window, sinks, max_rows, max_kv_len, out.data_ptr(), os_, _addr(lse),
           _addr(status), _addr(workspace), 0 if workspace is None else workspace.numel())

@@ -303,10 +303,11 @@ bool gemv_sizes_ok(int T, int K, int N, int group) {
 constexpr int kKv4MaxT = 1 << 22;
 constexpr int kKv4MaxB = 65536;
 constexpr int kKv4MaxHeads = 1024;
-// workgroups of the attention kernel that a call is split into, at least, where the cache is
-// long enough
-constexpr int kKv4TargetWgs = 1024;
-constexpr int kKv4MinSplitSteps = 8;  // steps of a split, at least: two for each wavefront
+// Workgroups of the attention kernel that run at once (256 compute units; two of 8 wavefronts
+// each where a workgroup holds 16 rows of up to 128, else one): the line of steps is cut into as
+// many parts.
+constexpr int kKv4Resident = 512;
+constexpr int kKv4MinSteps = 8;  // steps of a part, at least: one for each wavefront
 
 inline bool kv4_heads_ok(int Hkv, int D) {
   return Hkv >= 1 && Hkv <= kKv4MaxHeads && (D == 64 || D == 128 || D == 256);
@@ -318,30 +319,25 @@ inline bool kv4_page_ok(int D, int page_size, int group) {
 inline int log2_of(int v) { return 31 - __builtin_clz((unsigned)v); }
 
 struct Kv4Plan {
-  int nt, slots, S;
-  size_t part_bytes;  // of one split of one slot and head
+  int nt, slots, parts;
 };
-// rows: rows of a sequence at most; steps: steps of a row tile at most
-Kv4Plan plan_kv4(int T, int B, int Hq, int Hkv, int D, int rows, long long steps) {
+// parts of a head's steps: as many as run at once
+int kv4_parts(int Hkv, int D, int nt) {
+  const int wgs = nt == 1 && D <= 128 ? kKv4Resident : kKv4Resident / 2;
+  return std::max(wgs / Hkv, 1);
+}
+Kv4Plan plan_kv4(int T, int B, int Hq, int Hkv, int D, int rows) {
   const int r = Hq / Hkv;
   Kv4Plan p{};
   rows = std::max(std::min(rows, T), (T + B - 1) / B);
-  const long long heads_rows = (long long)rows * r;
   // one 16-row tile holds a token's heads; more rows share the decoded keys and values
-  p.nt = heads_rows <= 16 ? 1 : heads_rows <= 32 || D > 128 ? 2 : 4;
-  const int R = 16 * p.nt;
-  p.slots = (int)((long long)T * r / R) + B;
-  p.part_bytes = sizeof(float) * dqg::kv4_part_floats(p.nt, D);
-  const long long tiles = std::min<long long>(p.slots, B * ((heads_rows + R - 1) / R)) * Hkv;
-  p.S = 1;
-  if (tiles < kKv4TargetWgs)
-    p.S = (int)std::max(1LL, std::min((kKv4TargetWgs + tiles - 1) / tiles,
-                                      steps / kKv4MinSplitSteps));
+  p.nt = (long long)rows * r <= 16 || D > 128 ? 1 : 2;
+  p.slots = (int)((long long)T * r / (16 * p.nt)) + B;
+  p.parts = kv4_parts(Hkv, D, p.nt);
   return p;
 }
-long long kv4_steps(long long positions) {
-  return (positions + dqg::KV4_STEP - 1) / dqg::KV4_STEP;
-}
+// [counters, one a part][partials, two a part]
+size_t kv4_counter_bytes() { return sizeof(unsigned) * std::max(kKv4Resident, kKv4MaxHeads); }
 bool kv4_attn_sizes_ok(int T, int B, int Hq, int Hkv, int D) {
   return T >= 1 && T <= kKv4MaxT && B >= 1 && B <= kKv4MaxB && kv4_heads_ok(Hkv, D) && Hq >= 1 &&
          Hq % Hkv == 0 && Hq <= 65536 && (long long)T * Hq < (1LL << 30);
@@ -721,18 +717,12 @@ int kv4_read(uint16_t* k, uint16_t* v, int T, int64_t k_stride, int64_t v_stride
 
 size_t kv4_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int max_kv_len) {
   if (!kv4_attn_sizes_ok(T, B, Hq, Hkv, D) || max_kv_len < 1 || max_kv_len > (1 << 30)) return 0;
-  // a call's slots * Hkv * S is below 4 kKv4TargetWgs (it splits where its tiles, at least half
-  // the slots, are fewer than kKv4TargetWgs) and below slots * Hkv * steps / kKv4MinSplitSteps; the
-  // largest over the tile heights is monotonic in T, B and max_kv_len
+  if (max_kv_len <= kKv4MinSteps * dqg::KV4_STEP) return 0;
   size_t most = 0;
-  for (int nt = 1; nt <= (D > 128 ? 2 : 4); nt *= 2) {
-    const long long slots = (long long)T * (Hq / Hkv) / (16 * nt) + B;
-    const long long S = kv4_steps(max_kv_len) / kKv4MinSplitSteps;
-    if (S < 2) continue;
-    const long long parts = std::min(slots * Hkv * S, 4LL * kKv4TargetWgs);
-    most = std::max(most, (size_t)parts * sizeof(float) * dqg::kv4_part_floats(nt, D));
-  }
-  return up256(most);
+  for (int nt = 1; nt <= (D > 128 ? 1 : 2); ++nt)
+    most = std::max(most, 2 * (size_t)Hkv * kv4_parts(Hkv, D, nt) * sizeof(float) *
+                              dqg::kv4_part_floats(nt, D));
+  return up256(kv4_counter_bytes() + most);
 }
 
 int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32_t* cu_rows,
@@ -757,24 +747,20 @@ int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32
   const int most = max_kv_len ? std::min(max_kv_len, cap) : cap;
   if (workspace && workspace_bytes < kv4_attention_workspace_bytes(T, B, Hq, Hkv, D, most))
     return DQG_ERR_WORKSPACE;
-  const int rows = max_rows ? max_rows : T;
-  long long steps = kv4_steps(most);
-  if (window > 0)  // a tile of up to 64 rows sees `window` positions a row and the first ones
-    steps = std::min(steps, kv4_steps((long long)window + 64) + 1 + kv4_steps(sinks));
-  const Kv4Plan p = plan_kv4(T, B, Hq, Hkv, D, rows, steps);
+  const Kv4Plan p = plan_kv4(T, B, Hq, Hkv, D, max_rows ? max_rows : T);
   dqg::Kv4AttnArgs a{};
   a.w = kv4_where(T, B, cu_rows, kv_lens, block_table, max_pages, cache, num_pages, Hkv, D,
                   page_size, group, status);
   a.q = q; a.q_stride = q_stride; a.out = out; a.out_stride = out_stride; a.lse = lse;
-  a.part = static_cast<float*>(workspace);
   a.Hq = Hq; a.r = Hq / Hkv; a.scale = scale; a.window = window; a.sinks = sinks;
-  a.n_slots = p.slots; a.nt = p.nt;
-  a.S = 1;
-  if (workspace)  // (the query's bound; no call splits further than its workspace reaches)
-    a.S = (int)std::max<long long>(
-        1, std::min<long long>(p.S, (long long)(workspace_bytes / p.part_bytes) /
-                                        ((long long)p.slots * Hkv)));
-  if ((long long)p.slots * Hkv * a.S >= (1LL << 31) / (16 * p.nt)) return DQG_ERR_UNSUPPORTED;
+  a.n_slots = p.slots; a.nt = p.nt; a.n_parts = p.parts; a.min_steps = kKv4MinSteps;
+  // (places on the line are 32-bit)
+  if (workspace && (long long)p.slots * (cap / dqg::KV4_STEP) < (1LL << 30)) {
+    a.counters = static_cast<unsigned*>(workspace);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kv4_counter_bytes());
+  } else if ((long long)p.slots * Hkv >= (1LL << 31)) {
+    return DQG_ERR_UNSUPPORTED;
+  }
   return dqg::launch_kv4_attention(a, D, format, stream) == hipSuccess ? DQG_OK : DQG_ERR_HIP;
 }
 

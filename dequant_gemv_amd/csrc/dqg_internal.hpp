@@ -150,17 +150,20 @@ struct Kv4AttnArgs {
   int64_t q_stride, out_stride;
   uint16_t* out;
   float* lse;            // [T, Hq] or null
-  float* part;           // split partials (S > 1)
+  float* part;           // partial sums, two a part and head; null: tiles are not cut
+  unsigned* counters;    // [Hkv * n_parts], zero between calls
   int Hq, r;             // query heads, and query heads per kv head
   float scale;
   int window, sinks;
-  int n_slots, S, nt;    // row-tile slots, kv splits, 16-row tiles per workgroup
+  int n_slots, n_parts;  // row-tile slots; parts of a head's steps
+  int min_steps;         // steps of a part, at least
+  int nt;                // 16-row tiles per workgroup
 };
 constexpr int KV4_STEP = 32;  // tokens of one step of a wavefront
 hipError_t launch_kv4_write(const Kv4RowsArgs& a, int D, int fmt, hipStream_t st);
 hipError_t launch_kv4_read(const Kv4RowsArgs& a, int D, int fmt, hipStream_t st);
 hipError_t launch_kv4_attention(const Kv4AttnArgs& a, int D, int fmt, hipStream_t st);
-// bytes of one workgroup's partial: 16 nt rows of D sums, a maximum and a sum
+// floats of one partial: 16 nt rows of D sums, a maximum and a sum
 constexpr size_t kv4_part_floats(int nt, int D) { return (size_t)16 * nt * (D + 2); }
 
 }  // namespace dqg

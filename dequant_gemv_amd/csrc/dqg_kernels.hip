@@ -60,19 +60,6 @@ __host__ __device__ constexpr int sched_scratch_entries(int E) {
   return E <= 128 ? route_scratch(2) : route_scratch(8);
 }
 
-// Inclusive prefix sum over the 64 lanes with DPP: shifts by 1, 2, 4, 8 within each row of 16
-// lanes (lanes shifted in from outside the row add 0), then the last lane of row 0 into row 1
-// and of row 2 into row 3 (row_bcast:15), then lane 31 into rows 2 and 3 (row_bcast:31).
-__device__ __forceinline__ int wave_incl_sum(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
-  return v;
-}
-
 // exclusive prefix sums over experts of cnt (-> pos) by wave 0 (lane l takes experts
 // [l * per, l * per + per)); with `records`, active experts also get their records.
 // Returns the number of active experts in lane 63's s_nact.

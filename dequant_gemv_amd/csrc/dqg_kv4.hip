@@ -19,6 +19,7 @@
 namespace dqg {
 namespace {
 
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 
 constexpr float LOG2E = 1.4426950408889634f;
@@ -406,12 +407,11 @@ struct Tile {
   int p_lo, p_hi;            // positions of the first and last row
   int n_steps, sink_steps, main0;  // steps 0 .. sink_steps - 1, then main0, main0 + 1, ...
 };
-__device__ __forceinline__ bool tile_at(const Kv4AttnArgs& a, int slot, int head, int R, Tile& t) {
-  const Kv4Where& w = a.w;
+__device__ __forceinline__ bool tile_of(const Kv4AttnArgs& a, int b, int j, int head, int R,
+                                        Tile& t) {
   const int r = a.r;
-  t.b = seq_of_slot(w, slot, 1, [=](int c) { return (int)((int64_t)c * r / R); });
-  t.s = seq_at(w, t.b);
-  const int j = slot - ((int)((int64_t)t.s.row0 * r / R) + t.b);
+  t.b = b;
+  t.s = seq_at(a.w, b);
   t.head = head;
   t.rho0 = j * R;
   t.n_rho = min(R, t.s.n * r - t.rho0);
@@ -431,15 +431,27 @@ __device__ __forceinline__ bool tile_at(const Kv4AttnArgs& a, int slot, int head
   }
   return true;
 }
+__device__ __forceinline__ int position_of(const Tile& t, int step) {
+  return (step < t.sink_steps ? step : step - t.sink_steps + t.main0) * KV4_STEP;
+}
+// The tile of a slot: sequence b has floor(cu[b] r / R) + b .. as its first, which leaves room for
+// its ceil(n r / R) tiles.
+__device__ __forceinline__ bool tile_at(const Kv4AttnArgs& a, int slot, int head, int R, Tile& t) {
+  const int r = a.r;
+  const int b = seq_of_slot(a.w, slot, 1, [=](int c) { return (int)((int64_t)c * r / R); });
+  const int row0 = min(max(a.w.cu[b], 0), a.w.T);
+  return tile_of(a, b, slot - ((int)((int64_t)row0 * r / R) + b), head, R, t);
+}
 
 template <int D>
-struct Stage {  // one step's codes and scales of one lane
-  uint32_t kc[2][D / 32];
-  uint16_t ks[2][(D + 127) / 128];
-  uint32_t vc[D / 16];
-  uint4 vs[D / 64];
-  int t0;    // first position
-  bool ok;   // the page exists
+struct KStage {  // one step's K codes and scales of one lane
+  uint32_t c[2][D / 32];
+  uint16_t s[2][(D + 127) / 128];
+};
+template <int D>
+struct VStage {
+  uint32_t c[D / 16];
+  uint4 s[D / 64];
 };
 
 template <int D>
@@ -464,43 +476,47 @@ struct Offsets {  // per lane, inside a head's part of a page, for position 0
   }
 };
 
+// Where a step's 32 positions lie: the head's part of their page, and the byte offsets of the
+// step's codes and scales in it.
+struct Place {
+  const uint8_t* codes;
+  const uint8_t* scales;
+};
 template <int D>
-__device__ __forceinline__ void load_stage(const Kv4AttnArgs& a, const Tile& t, int step,
-                                           const Offsets<D>& off, Stage<D>& x) {
-  const Kv4Where& w = a.w;
-  const int j = step < t.sink_steps ? step : step - t.sink_steps + t.main0;
-  x.t0 = j * KV4_STEP;
-  const int page = __builtin_amdgcn_readfirstlane(
-      w.table[(int64_t)t.b * w.max_pages + (x.t0 >> w.page_shift)]);
-  x.ok = page >= 0 && page < w.num_pages;
-  const int in_page = x.t0 & ((1 << w.page_shift) - 1);
+__device__ __forceinline__ Place place_of(const Kv4Where& w, int head, int page, int t0) {
+  const int in_page = t0 & ((1 << w.page_shift) - 1);
   const int n_shift = (D == 64 ? 6 : D == 128 ? 7 : 8) - w.group_shift;
-  const uint8_t* base = w.cache + (x.ok ? page : 0) * w.page_bytes + (int64_t)t.head * w.head_bytes;
-  const uint8_t* codes = base + in_page * (D / 2);
-  const uint8_t* scales = base + ((in_page << n_shift) << 1);
+  const uint8_t* base = w.cache + page * w.page_bytes + (int64_t)head * w.head_bytes;
+  return {base + in_page * (D / 2), base + ((in_page << n_shift) << 1)};
+}
+template <int D>
+__device__ __forceinline__ void load_k(const Place& p, const Offsets<D>& off, KStage<D>& x) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     if constexpr (D == 64) {
-      const uint2 c = *reinterpret_cast<const uint2*>(codes + off.kc[h]);
-      x.kc[h][0] = c.x;
-      x.kc[h][1] = c.y;
+      const uint2 c = *reinterpret_cast<const uint2*>(p.codes + off.kc[h]);
+      x.c[h][0] = c.x;
+      x.c[h][1] = c.y;
     } else {
 #pragma unroll
       for (int c = 0; c < D / 128; ++c) {
-        const uint4 u = *reinterpret_cast<const uint4*>(codes + off.kc[h] + 64 * c);
-        x.kc[h][4 * c] = u.x; x.kc[h][4 * c + 1] = u.y;
-        x.kc[h][4 * c + 2] = u.z; x.kc[h][4 * c + 3] = u.w;
+        const uint4 u = *reinterpret_cast<const uint4*>(p.codes + off.kc[h] + 64 * c);
+        x.c[h][4 * c] = u.x; x.c[h][4 * c + 1] = u.y;
+        x.c[h][4 * c + 2] = u.z; x.c[h][4 * c + 3] = u.w;
       }
     }
 #pragma unroll
     for (int c = 0; c < (D + 127) / 128; ++c)
-      x.ks[h][c] = *reinterpret_cast<const uint16_t*>(scales + off.ks[h][c]);
+      x.s[h][c] = *reinterpret_cast<const uint16_t*>(p.scales + off.ks[h][c]);
   }
+}
+template <int D>
+__device__ __forceinline__ void load_v(const Place& p, const Offsets<D>& off, VStage<D>& x) {
 #pragma unroll
   for (int c = 0; c < D / 64; ++c) {
-    const uint4 u = *reinterpret_cast<const uint4*>(codes + off.vc + 256 * c);
-    x.vc[4 * c] = u.x; x.vc[4 * c + 1] = u.y; x.vc[4 * c + 2] = u.z; x.vc[4 * c + 3] = u.w;
-    x.vs[c] = *reinterpret_cast<const uint4*>(scales + off.vs[c]);
+    const uint4 u = *reinterpret_cast<const uint4*>(p.codes + off.vc + 256 * c);
+    x.c[4 * c] = u.x; x.c[4 * c + 1] = u.y; x.c[4 * c + 2] = u.z; x.c[4 * c + 3] = u.w;
+    x.s[c] = *reinterpret_cast<const uint4*>(p.scales + off.vs[c]);
   }
 }
 
@@ -533,92 +549,133 @@ __host__ __device__ constexpr int value_at(int i) {
   return FMT == FMT_INT4 ? (i >> 1) + 4 * (i & 1) : i;
 }
 
+// Query rows of one (sequence, head): lane (q, g) holds row q of each 16-row tile as the B operand
+// of S^T, the d of K dword i in that dword's value order, and its row's position.
+template <int D, int NT>
+struct Queries {
+  f16x8_t q[NT][D / 32];
+  int pos[NT];
+};
 template <int D, int FMT, int NT>
+__device__ __forceinline__ void load_queries(const Kv4AttnArgs& a, const Tile& t, int q16, int g,
+                                             Queries<D, NT>& x) {
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const int rho = t.rho0 + 16 * nt + q16;
+    const bool on = 16 * nt + q16 < t.n_rho;
+    const int i = rho / a.r, h = t.head * a.r + rho % a.r;
+    x.pos[nt] = on ? t.s.len - t.s.n + i : -1;
+    const uint16_t* p = a.q + (int64_t)(t.s.row0 + i) * a.q_stride + (int64_t)h * D;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      const int d0 = D == 64 ? 16 * g + 8 * j : 128 * (j / 4) + 32 * g + 8 * (j % 4);
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (on) u = *reinterpret_cast<const uint4*>(p + d0);
+      const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int d = value_at<FMT>(e);
+        x.q[nt][j][e] = (_Float16)((d & 1) ? bf16_hi(uw[d / 2]) : bf16_lo(uw[d / 2]));
+      }
+    }
+  }
+}
+
+template <int D, int NT>
 struct Acc {
   f32x4_t o[NT][D / 64][4];
   float m[NT], l[NT];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt] = -FLT_MAX;
+      l[nt] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e)
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) o[nt][e][jj] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+  }
 };
 
+// Scores of a step's 32 positions, in powers of 2.
 template <int D, int FMT, int NT>
-__device__ __forceinline__ void attn_step(const Kv4AttnArgs& a, const Tile& t, const Stage<D>& x,
-                                          const f16x8_t (&q)[NT][D / 32], const int (&pos)[NT],
-                                          float c, int g, Acc<D, FMT, NT>& acc) {
-  if (!x.ok) return;
-  f32x4_t sc[NT][2];
+__device__ __forceinline__ void step_scores(const KStage<D>& x, const Queries<D, NT>& q, float c,
+                                            f32x4_t (&sc)[NT][2]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) sc[nt][h] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      const _Float16 s1 = (_Float16)bf16_to_f32(x.ks[h][D == 64 ? 0 : i / 4]);
+      const _Float16 s1 = (_Float16)bf16_to_f32(x.s[h][D == 64 ? 0 : i / 4]);
       const f16x2_t s = {s1, s1};
       const f16x2_t s24 = s * (f16x2_t){(_Float16)-24.0f, (_Float16)-24.0f};
       const f16x2_t s4[4] = {s, s, s, s}, z4[4] = {s24, s24, s24, s24};
-      const f16x8_t k = decode_f16<FMT>(x.kc[h][i], s4, z4);
+      const f16x8_t k = decode_f16<FMT>(x.c[h][i], s4, z4);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
-        sc[nt][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[nt][i], sc[nt][h], 0, 0, 0);
+        sc[nt][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q.q[nt][i], sc[nt][h], 0, 0, 0);
     }
   }
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)  // scores in powers of 2
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int h = 0; h < 2; ++h) sc[nt][h] *= c;
-  // V scales of the lane's 8 positions, two groups' worth at most per 64 columns
-  f16x2_t vs[D / 64][4], vs24[D / 64][4];
+}
+
+// Steps with positions that some row does not see.  What lies there may be anything: scores are
+// replaced and V scales cleared.  A position whose V scale is not finite and that only some rows
+// see is cleared too, and the rows that see it get a NaN score.
+template <int D, int NT>
+__device__ __forceinline__ void step_mask(const Kv4AttnArgs& a, const Tile& t, int t0, int g,
+                                          const Queries<D, NT>& q, f32x4_t (&sc)[NT][2],
+                                          uint4 (&vs)[D / 64]) {
   uint32_t vw[D / 64][4];
 #pragma unroll
   for (int e = 0; e < D / 64; ++e) {
-    vw[e][0] = x.vs[e].x; vw[e][1] = x.vs[e].y; vw[e][2] = x.vs[e].z; vw[e][3] = x.vs[e].w;
+    vw[e][0] = vs[e].x; vw[e][1] = vs[e].y; vw[e][2] = vs[e].z; vw[e][3] = vs[e].w;
   }
-  const bool edge = x.t0 + KV4_STEP - 1 > t.p_lo ||
-                    (a.window > 0 && x.t0 <= t.p_hi - a.window && x.t0 + KV4_STEP > a.sinks);
-  if (edge) {
-    // hidden positions may hold anything: their scores are replaced and their V scales cleared.
-    // A position with a non-finite V scale that only some rows see is cleared too, and the rows
-    // that see it get a NaN score.
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int p = x.t0 + 8 * g + i;
-      bool bad = false;
+  for (int i = 0; i < 8; ++i) {
+    const int p = t0 + 8 * g + i;
+    bool bad = false;
 #pragma unroll
-      for (int e = 0; e < D / 64; ++e) {
-        const uint32_t b16 = (i & 1) ? vw[e][i / 2] >> 16 : vw[e][i / 2] & 0xFFFFu;
-        bad |= (b16 & 0x7F80u) == 0x7F80u;
-      }
-      const uint64_t bads = __ballot(bad);
-      const bool poisoned = ((bads >> (16 * g)) & 0xFFFFu) != 0;
-      if (poisoned || p > t.p_hi)
+    for (int e = 0; e < D / 64; ++e) {
+      const uint32_t b16 = (i & 1) ? vw[e][i / 2] >> 16 : vw[e][i / 2] & 0xFFFFu;
+      bad |= (b16 & 0x7F80u) == 0x7F80u;
+    }
+    const uint64_t bads = __ballot(bad);
+    const bool poisoned = ((bads >> (16 * g)) & 0xFFFFu) != 0;
+    if (poisoned || p > t.p_hi)
 #pragma unroll
-        for (int e = 0; e < D / 64; ++e)
-          vw[e][i / 2] &= (i & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+      for (int e = 0; e < D / 64; ++e) vw[e][i / 2] &= (i & 1) ? 0x0000FFFFu : 0xFFFF0000u;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const bool seen = p <= pos[nt] &&
-                          (a.window == 0 || p > pos[nt] - a.window || p < a.sinks);
-        const float s = sc[nt][i >> 2][i & 3];
-        sc[nt][i >> 2][i & 3] = !seen ? -INFINITY : poisoned ? NAN : s;
-      }
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool seen = p <= q.pos[nt] &&
+                        (a.window == 0 || p > q.pos[nt] - a.window || p < a.sinks);
+      const float s = sc[nt][i >> 2][i & 3];
+      sc[nt][i >> 2][i & 3] = !seen ? -INFINITY : poisoned ? NAN : s;
     }
   }
 #pragma unroll
-  for (int e = 0; e < D / 64; ++e)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int i0 = value_at<FMT>(2 * i), i1 = value_at<FMT>(2 * i + 1);
-      const float s0 = (i0 & 1) ? bf16_hi(vw[e][i0 / 2]) : bf16_lo(vw[e][i0 / 2]);
-      const float s1 = (i1 & 1) ? bf16_hi(vw[e][i1 / 2]) : bf16_lo(vw[e][i1 / 2]);
-      vs[e][i] = f16x2_t{(_Float16)s0, (_Float16)s1};
-      vs24[e][i] = vs[e][i] * (f16x2_t){(_Float16)-24.0f, (_Float16)-24.0f};
-    }
-  // the reference moves where one passes it by more than MOVE
+  for (int e = 0; e < D / 64; ++e) vs[e] = make_uint4(vw[e][0], vw[e][1], vw[e][2], vw[e][3]);
+}
+__device__ __forceinline__ bool step_at_edge(const Kv4AttnArgs& a, const Tile& t, int t0) {
+  return t0 + KV4_STEP - 1 > t.p_lo ||
+         (a.window > 0 && t0 <= t.p_hi - a.window && t0 + KV4_STEP > a.sinks);
+}
+
+// Scores -> weights: the reference maximum moves where a score passes it by more than MOVE.
+template <int D, int FMT, int NT>
+__device__ __forceinline__ void step_weights(const f32x4_t (&sc)[NT][2], Acc<D, NT>& acc,
+                                             f16x8_t (&p)[NT]) {
   bool move = false;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    float mx = -INFINITY;
+    float mx = sc[nt][0][0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) mx = fmaxf(mx, sc[nt][i >> 2][i & 3]);
+    for (int i = 1; i < 8; ++i) mx = fmaxf(mx, sc[nt][i >> 2][i & 3]);
     move |= mx > acc.m[nt] + MOVE;
   }
   if (__ballot(move)) {
@@ -638,228 +695,343 @@ __device__ __forceinline__ void attn_step(const Kv4AttnArgs& a, const Tile& t, c
         for (int jj = 0; jj < 4; ++jj) acc.o[nt][e][jj] *= f;
     }
   }
-  f16x8_t p[NT];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    float v[8], sum = 0.0f;
+    const float ref = acc.m[nt] - P_SHIFT;
+    float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = __builtin_amdgcn_exp2f(sc[nt][i >> 2][i & 3] - (acc.m[nt] - P_SHIFT));
-      sum += v[i];
-    }
-    acc.l[nt] += sum;
+    for (int i = 0; i < 8; ++i) v[i] = __builtin_amdgcn_exp2f(sc[nt][i >> 2][i & 3] - ref);
+    acc.l[nt] += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
 #pragma unroll
     for (int i = 0; i < 8; ++i) p[nt][i] = (_Float16)v[value_at<FMT>(i)];
   }
-#pragma unroll
-  for (int e = 0; e < D / 64; ++e)
-#pragma unroll
-    for (int jj = 0; jj < 4; ++jj) {
-      const f16x8_t v = decode_f16<FMT>(x.vc[4 * e + jj], vs[e], vs24[e]);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        acc.o[nt][e][jj] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[nt], acc.o[nt][e][jj], 0, 0, 0);
-    }
 }
 
-// Splits of a tile: `per` steps each, the last shorter.
-__device__ __forceinline__ int steps_per_split(int n_steps, int S) {
-  return max((n_steps + S - 1) / S, 1);
+// O^T += V^T P^T
+template <int D, int FMT, int NT>
+__device__ __forceinline__ void step_values(const VStage<D>& x, const f16x8_t (&p)[NT],
+                                            Acc<D, NT>& acc) {
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e) {
+    const uint32_t w[4] = {x.s[e].x, x.s[e].y, x.s[e].z, x.s[e].w};
+    f16x2_t s[4], s24[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int i0 = value_at<FMT>(2 * i), i1 = value_at<FMT>(2 * i + 1);
+      s[i] = f16x2_t{(_Float16)((i0 & 1) ? bf16_hi(w[i0 / 2]) : bf16_lo(w[i0 / 2])),
+                     (_Float16)((i1 & 1) ? bf16_hi(w[i1 / 2]) : bf16_lo(w[i1 / 2]))};
+      s24[i] = s[i] * (f16x2_t){(_Float16)-24.0f, (_Float16)-24.0f};
+    }
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj) {
+      const f16x8_t v = decode_f16<FMT>(x.c[4 * e + jj], s, s24);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        acc.o[nt][e][jj] =
+            __builtin_amdgcn_mfma_f32_16x16x32_f16(v, p[nt], acc.o[nt][e][jj], 0, 0, 0);
+    }
+  }
 }
 
 // One row of the result: o = sum / l (zero where nothing was visible), lse = ln(sum of exp).
+__device__ __forceinline__ float row_inv(float l) { return l > 0.0f || l != l ? 1.0f / l : 0.0f; }
 __device__ __forceinline__ float row_lse(float m, float l) {
   return l > 0.0f || l != l ? (m - P_SHIFT) * LN2 + logf(l) : -INFINITY;
 }
 
-// One workgroup per (row tile, kv split, kv head); its 4 wavefronts take the split's steps in
-// turn and join their sums through LDS in a fixed order.
-template <int D, int FMT, int NT>
-__global__ __launch_bounds__(256) void kv4_attn_kernel(Kv4AttnArgs a) {
-  constexpr int R = 16 * NT, LD = D + 4;
-  __shared__ float lds_o[3][16][LD];
-  __shared__ float lds_m[4][R], lds_l[4][R];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int q16 = lane & 15, g = lane >> 4;
-  const int head = blockIdx.x % a.w.Hkv, rest = blockIdx.x / a.w.Hkv;
-  const int split = rest % a.S, slot = a.n_slots - 1 - rest / a.S;
-  Tile t;
-  if (!tile_at(a, slot, head, R, t)) return;
-  if (t.s.len > t.s.cap && split == 0 && threadIdx.x == 0) report(a.w.status, ST_LENGTH);
-  const int per = steps_per_split(t.n_steps, a.S);
-  const int s0 = split * per, s1 = min(s0 + per, t.n_steps);
-  if (split > 0 && s0 >= t.n_steps) return;
+// ---- attention of few rows over long caches -------------------------------------------------
+// The steps of all row tiles of a head, in order of sequence and tile, are one line that is cut
+// into equal parts, one workgroup each: ragged batches, single long caches and many short ones
+// load the GPU evenly, in one round of workgroups.  A part's wavefronts take its steps in turn and
+// join through LDS; a tile that a cut goes through leaves partial sums, and the workgroup that
+// finishes last joins them in order of position.
+constexpr int ROWS_WAVES = 8;
 
-  // Q^T operands: lane (q, g) holds the d of K dword i of chunk i / 4 in that dword's value order
-  f16x8_t q[NT][D / 32];
-  int pos[NT];
+// Tiles of a sequence and (an upper bound of) the steps of each; a tile that sees nothing counts
+// one step, so that its rows are written.
+__device__ __forceinline__ void seq_work(const Kv4AttnArgs& a, const Seq& s, int R, int* tiles,
+                                         int* steps) {
+  *tiles = (int)(((int64_t)s.n * a.r + R - 1) / R);
+  const int end = min(s.len, s.cap);
+  int w = (end + KV4_STEP - 1) / KV4_STEP;
+  if (a.window > 0) {
+    const int rows = (R + a.r - 2) / a.r + 1;  // rows of a tile, at most
+    const int main = (a.window - 1 + rows + 2 * KV4_STEP - 2) / KV4_STEP;
+    const int first = (min(a.sinks, end) + KV4_STEP - 1) / KV4_STEP;
+    if (main + first > 0) w = min(w, main + first);
+  }
+  *steps = max(w, 1);
+}
+struct Spot {  // a place on the line
+  int b, tile, steps;  // sequence, its tile, steps of each of its tiles
+  int start;           // where the tile starts
+};
+// The tile that holds place x (x < total), or with x < 0 the line's length in start.
+__device__ __forceinline__ Spot find_spot(const Kv4AttnArgs& a, int R, int x) {
+  const int lane = threadIdx.x & 63;
+  Spot f{0, 0, 1, 0};
+  int before = 0;
+  for (int b0 = 0; b0 < a.w.B; b0 += 64) {
+    int tiles = 0, steps = 1;
+    if (b0 + lane < a.w.B) seq_work(a, seq_at(a.w, b0 + lane), R, &tiles, &steps);
+    const int mine = tiles * steps;
+    const int incl = wave_incl_sum(mine);
+    const int all = __builtin_amdgcn_readlane(incl, 63);
+    if (x >= 0 && x < before + all) {
+      const int i = __popcll(__ballot(before + incl <= x));
+      const int s0 = before + __builtin_amdgcn_readlane(incl - mine, i);
+      f.b = b0 + i;
+      f.steps = __builtin_amdgcn_readlane(steps, i);
+      f.tile = (x - s0) / f.steps;
+      f.start = s0 + f.tile * f.steps;
+      return f;
+    }
+    before += all;
+  }
+  f.start = before;
+  return f;
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t part_rsrc(const float* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p), 0, 0x7FFFFFFF, 0x00020000);
+}
+// 16-byte accesses that other workgroups of the launch see (sc1: past the XCD's L2)
+__device__ __forceinline__ void st4_agent(__amdgpu_buffer_rsrc_t r, int word, float4 v) {
+  const u32x4_t d = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z),
+                     __float_as_uint(v.w)};
+  __builtin_amdgcn_raw_buffer_store_b128(d, r, word * 4, 0, 16);
+}
+__device__ __forceinline__ float4 ld4_agent(__amdgpu_buffer_rsrc_t r, int word) {
+  const u32x4_t d = __builtin_amdgcn_raw_buffer_load_b128(r, word * 4, 0, 16);
+  return make_float4(__uint_as_float(d.x), __uint_as_float(d.y), __uint_as_float(d.z),
+                     __uint_as_float(d.w));
+}
+
+// Output of 4 columns of one row.
+__device__ __forceinline__ void store_out4(const Kv4AttnArgs& a, const Tile& t, int D, int row, int d,
+                                           float4 v, float inv) {
+  const int rho = t.rho0 + row, qi = t.s.row0 + rho / a.r, h = t.head * a.r + rho % a.r;
+  const bf16x2_t lo = {(__bf16)(v.x * inv), (__bf16)(v.y * inv)};
+  const bf16x2_t hi = {(__bf16)(v.z * inv), (__bf16)(v.w * inv)};
+  *reinterpret_cast<uint2*>(a.out + (int64_t)qi * a.out_stride + (int64_t)h * D + d) =
+      make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+}
+__device__ __forceinline__ void store_lse(const Kv4AttnArgs& a, const Tile& t, int row, float m,
+                                          float l) {
+  const int rho = t.rho0 + row, qi = t.s.row0 + rho / a.r, h = t.head * a.r + rho % a.r;
+  if (a.lse) a.lse[(int64_t)qi * a.Hq + h] = row_lse(m, l);
+}
+
+// Joins the partials of one tile: parts first .. first + n - 1 of this head; the first left its
+// sums in its second place (the tile ends behind the part), the others in their first.  A
+// wavefront takes a row at a time; LR lanes hold a row, so it reads 64 / LR parts at once.
+template <int D, int R>
+__device__ __forceinline__ void join_parts(const Kv4AttnArgs& a, const Tile& t, int part0, int first,
+                                           int n, int wave, int n_waves) {
+  constexpr int LR = D / 4, PL = 64 / LR, SIZE = R * (D + 2);
+  const int lane = threadIdx.x & 63, sub = lane / LR, d = 4 * (lane % LR);
+  const __amdgpu_buffer_rsrc_t r = part_rsrc(a.part);
+  for (int row = wave; row < t.n_rho; row += n_waves) {
+    float m = -FLT_MAX, l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k0 = 0; k0 < n; k0 += 64) {
+      const int k = k0 + lane;
+      float pm = -FLT_MAX, pl = 0.0f;
+      if (k < n) {
+        const int at = (2 * (part0 + first + k) + (k == 0)) * SIZE + R * D + row;
+        pm = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at * 4, 0, 16));
+        pl = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (at + R) * 4, 0, 16));
+      }
+      float mx = pm;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int rho = t.rho0 + 16 * nt + q16;
-    const bool on = 16 * nt + q16 < t.n_rho;
-    const int i = rho / a.r, h = t.head * a.r + rho % a.r;
-    pos[nt] = on ? t.s.len - t.s.n + i : -1;
-    const uint16_t* p = a.q + (int64_t)(t.s.row0 + i) * a.q_stride + (int64_t)h * D;
-#pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-      const int d0 = D == 64 ? 16 * g + 8 * j : 128 * (j / 4) + 32 * g + 8 * (j % 4);
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (on) u = *reinterpret_cast<const uint4*>(p + d0);
-      const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int d = value_at<FMT>(e);
-        q[nt][j][e] = (_Float16)((d & 1) ? bf16_hi(uw[d / 2]) : bf16_lo(uw[d / 2]));
+      for (int i = 1; i < 64; i *= 2) mx = fmaxf(mx, __shfl_xor(mx, i));
+      mx = fmaxf(mx, m);
+      const float f0 = __builtin_amdgcn_exp2f(m - mx);
+      m = mx;
+      const float f = __builtin_amdgcn_exp2f(pm - m);
+      l = l * f0 + f * pl;
+      o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
+      const int here = min(n - k0, 64);
+#pragma unroll 8
+      for (int j = 0; j < here; j += PL) {
+        const int kk = min(j + sub, here - 1);
+        const float4 v = ld4_agent(r, (2 * (part0 + first + k0 + kk) + (k0 + kk == 0)) * SIZE +
+                                          row * D + d);
+        float fk = __shfl(f, kk);  // (every lane takes part)
+        fk = j + sub < here ? fk : 0.0f;
+        o.x += fk * v.x; o.y += fk * v.y; o.z += fk * v.z; o.w += fk * v.w;
       }
     }
+#pragma unroll
+    for (int i = 1; i < 64; i *= 2) l += __shfl_xor(l, i);
+#pragma unroll
+    for (int i = LR; i < 64; i *= 2) {
+      o.x += __shfl_xor(o.x, i); o.y += __shfl_xor(o.y, i);
+      o.z += __shfl_xor(o.z, i); o.w += __shfl_xor(o.w, i);
+    }
+    if (sub == 0) store_out4(a, t, D, row, d, o, row_inv(l));
+    if (lane == 0) store_lse(a, t, row, m, l);
   }
-  Acc<D, FMT, NT> acc;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    acc.m[nt] = -FLT_MAX;
-    acc.l[nt] = 0.0f;
-#pragma unroll
-    for (int e = 0; e < D / 64; ++e)
-#pragma unroll
-      for (int jj = 0; jj < 4; ++jj) acc.o[nt][e][jj] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
+template <int D, int FMT, int NT>
+__global__ __launch_bounds__(64 * ROWS_WAVES, NT == 1 && D <= 128 ? 4 : 2) void kv4_attn_rows_kernel(Kv4AttnArgs a) {
+  constexpr int R = 16 * NT, LD = D + 4, NW = ROWS_WAVES, SIZE = R * (D + 2);
+  __shared__ float lds_o[NW][16][LD];
+  __shared__ float lds_m[NW][R], lds_l[NW][R];
+  __shared__ int lds_flag;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q16 = lane & 15, g = lane >> 4;
+  const int head = blockIdx.x % a.w.Hkv, part = blockIdx.x / a.w.Hkv;
+  const int part0 = head * a.n_parts;
+  const bool cut = a.part != nullptr;  // without partials a part is a whole tile
+  int x, end, per = 1;
+  Spot spot;
+  if (cut) {
+    const int total = find_spot(a, R, -1).start;
+    per = max((total + a.n_parts - 1) / a.n_parts, a.min_steps);
+    per = (per + NW - 1) / NW * NW;  // a shorter part takes a wavefront as long
+    x = part * per;
+    end = min(x + per, total);
+    if (x >= end) return;
+    spot = find_spot(a, R, x);
   }
+  Tile t;
   const float c = a.scale * LOG2E;
   const Offsets<D> off(a.w, lane);
-  bool all_ok = true;
-  int step = s0 + wave;
-  if (step < s1) {
-    Stage<D> x, y;
-    load_stage<D>(a, t, step, off, x);
-    while (true) {
-      const bool more = step + 4 < s1;
-      if (more) load_stage<D>(a, t, step + 4, off, y);
-      all_ok &= x.ok;
-      attn_step<D, FMT, NT>(a, t, x, q, pos, c, g, acc);
-      if (!more) break;
-      step += 4;
-      x = y;
+  while (true) {
+    int s0 = 0, s1;
+    bool whole = true;
+    if (cut) {
+      tile_of(a, spot.b, spot.tile, head, R, t);
+      s0 = x - spot.start;
+      s1 = min(end - spot.start, spot.steps);
+      whole = s0 == 0 && s1 == spot.steps;
+    } else {
+      if (!tile_at(a, part, head, R, t)) return;
+      s1 = t.n_steps;
     }
-  }
-  if (!all_ok && lane == 0) report(a.w.status, ST_PAGE);
+    if (t.s.len > t.s.cap && s0 == 0 && threadIdx.x == 0) report(a.w.status, ST_LENGTH);
+    Queries<D, NT> q;
+    load_queries<D, FMT, NT>(a, t, q16, g, q);
+    Acc<D, NT> acc;
+    acc.clear();
+    bool all_ok = true;
+    const int last = min(s1, t.n_steps);
+    for (int base = s0 + wave; base < last; base += 64 * NW) {
+      // pages of up to 64 of the wavefront's steps, one a lane; -1: no such page
+      int pages;
+      {
+        const int step = min(base + lane * NW, last - 1);
+        pages = a.w.table[(int64_t)t.b * a.w.max_pages + (position_of(t, step) >> a.w.page_shift)];
+        if (pages < 0 || pages >= a.w.num_pages) pages = -1;
+      }
+      const int n = min((last - base + NW - 1) / NW, 64);
+      KStage<D> ks;
+      VStage<D> vs;
+      int t0 = position_of(t, base);
+      int page = __builtin_amdgcn_readlane(pages, 0);
+      Place pl = place_of<D>(a.w, head, max(page, 0), t0);
+      load_k<D>(pl, off, ks);
+      load_v<D>(pl, off, vs);
+      for (int i = 0; i < n; ++i) {
+        const bool more = i + 1 < n;
+        const int t0n = position_of(t, min(base + (i + 1) * NW, last - 1));
+        const int pagen = __builtin_amdgcn_readlane(pages, min(i + 1, n - 1));
+        const Place pln = place_of<D>(a.w, head, max(pagen, 0), t0n);
+        f32x4_t sc[NT][2];
+        step_scores<D, FMT, NT>(ks, q, c, sc);
+        if (more) load_k<D>(pln, off, ks);
+        if (page >= 0) {
+          if (step_at_edge(a, t, t0)) step_mask<D, NT>(a, t, t0, g, q, sc, vs.s);
+          f16x8_t p[NT];
+          step_weights<D, FMT, NT>(sc, acc, p);
+          step_values<D, FMT, NT>(vs, p, acc);
+        } else {
+          all_ok = false;
+        }
+        if (more) load_v<D>(pln, off, vs);
+        t0 = t0n;
+        page = pagen;
+      }
+    }
+    if (!all_ok && lane == 0) report(a.w.status, ST_PAGE);
 
+    // join the wavefronts: sums to LDS, then each wavefront adds two rows of every 16
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    float l = acc.l[nt];
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
-    if (g == 0) {
-      lds_m[wave][16 * nt + q16] = acc.m[nt];
-      lds_l[wave][16 * nt + q16] = l;
+    for (int nt = 0; nt < NT; ++nt) {
+      float l = acc.l[nt];
+      l += __shfl_xor(l, 16);
+      l += __shfl_xor(l, 32);
+      if (g == 0) {
+        lds_m[wave][16 * nt + q16] = acc.m[nt];
+        lds_l[wave][16 * nt + q16] = l;
+      }
     }
-  }
-  __syncthreads();
-  const bool whole = per >= t.n_steps;  // this split is the tile's only one
-  float* part = whole ? nullptr
-                      : a.part + (((int64_t)slot * a.w.Hkv + head) * a.S + split) *
-                                     (int64_t)(R * (D + 2));
+    const int place = 2 * (part0 + part) + (s0 == 0);
+    const __amdgpu_buffer_rsrc_t pr = part_rsrc(a.part);
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int row = 16 * nt + q16;
-    float m = lds_m[0][row];
-#pragma unroll
-    for (int w = 1; w < 4; ++w) m = fmaxf(m, lds_m[w][row]);
-    float l = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) l += lds_l[w][row] * __builtin_amdgcn_exp2f(lds_m[w][row] - m);
-    const float f = __builtin_amdgcn_exp2f(acc.m[nt] - m);
-    if (nt > 0) __syncthreads();
-    // wavefront nt collects: the others leave their sums in LDS, lower wavefronts first
-    if (wave != nt) {
-      float* dst = &lds_o[wave < nt ? wave : wave - 1][q16][0];
+    for (int nt = 0; nt < NT; ++nt) {
+      if (nt > 0) __syncthreads();
+      float* dst = &lds_o[wave][q16][0];
 #pragma unroll
       for (int e = 0; e < D / 64; ++e)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<float4*>(dst + 64 * e + 16 * g + 4 * i) =
-              make_float4(acc.o[nt][e][0][i] * f, acc.o[nt][e][1][i] * f, acc.o[nt][e][2][i] * f,
-                          acc.o[nt][e][3][i] * f);
-    }
-    __syncthreads();
-    if (wave == nt && row < t.n_rho) {
-      const int rho = t.rho0 + row, qi = t.s.row0 + rho / a.r, h = t.head * a.r + rho % a.r;
-      const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-      uint16_t* out = a.out + (int64_t)qi * a.out_stride + (int64_t)h * D;
+              make_float4(acc.o[nt][e][0][i], acc.o[nt][e][1][i], acc.o[nt][e][2][i],
+                          acc.o[nt][e][3][i]);
+      __syncthreads();
 #pragma unroll
-      for (int e = 0; e < D / 64; ++e) {
-        float v[16];
+      for (int rr = 0; rr < 16 / NW; ++rr) {
+        const int row16 = (16 / NW) * wave + rr, row = 16 * nt + row16;
+        if (row < t.n_rho) {
+          float m = lds_m[0][row];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float4 u = make_float4(acc.o[nt][e][0][i] * f, acc.o[nt][e][1][i] * f,
-                                 acc.o[nt][e][2][i] * f, acc.o[nt][e][3][i] * f);
+          for (int w = 1; w < NW; ++w) m = fmaxf(m, lds_m[w][row]);
+          float l = 0.0f, f[NW];
 #pragma unroll
-          for (int w = 0; w < 3; ++w) {
-            const float4 z = *reinterpret_cast<const float4*>(&lds_o[w][q16][64 * e + 16 * g + 4 * i]);
-            u.x += z.x; u.y += z.y; u.z += z.z; u.w += z.w;
+          for (int w = 0; w < NW; ++w) {
+            f[w] = __builtin_amdgcn_exp2f(lds_m[w][row] - m);
+            l += lds_l[w][row] * f[w];
           }
-          v[4 * i] = u.x; v[4 * i + 1] = u.y; v[4 * i + 2] = u.z; v[4 * i + 3] = u.w;
-        }
-        if (whole) {
-          uint32_t b[8];
+          const int d = 4 * lane;
+          if (d < D) {
+            float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const bf16x2_t hh = {(__bf16)(v[2 * i] * inv), (__bf16)(v[2 * i + 1] * inv)};
-            b[i] = __builtin_bit_cast(uint32_t, hh);
+            for (int w = 0; w < NW; ++w) {
+              const float4 z = *reinterpret_cast<const float4*>(&lds_o[w][row16][d]);
+              u.x += f[w] * z.x; u.y += f[w] * z.y; u.z += f[w] * z.z; u.w += f[w] * z.w;
+            }
+            if (whole)
+              store_out4(a, t, D, row, d, u, row_inv(l));
+            else
+              st4_agent(pr, place * SIZE + row * D + d, u);
           }
-          uint4* dst = reinterpret_cast<uint4*>(out + 64 * e + 16 * g);
-          dst[0] = make_uint4(b[0], b[1], b[2], b[3]);
-          dst[1] = make_uint4(b[4], b[5], b[6], b[7]);
-        } else {
-          float4* dst = reinterpret_cast<float4*>(part + row * D + 64 * e + 16 * g);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            dst[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-        }
-      }
-      if (g == 0) {
-        if (!whole) {
-          part[R * D + row] = m;
-          part[R * D + R + row] = l;
-        } else if (a.lse) {
-          a.lse[(int64_t)qi * a.Hq + h] = row_lse(m, l);
+          if (lane == 0) {
+            if (whole) {
+              store_lse(a, t, row, m, l);
+            } else {
+              st_sc1(a.part, (size_t)place * SIZE + R * D + row, m);
+              st_sc1(a.part, (size_t)place * SIZE + R * D + R + row, l);
+            }
+          }
         }
       }
     }
+    if (!cut) return;
+    if (!whole) {
+      const int first = spot.start / per, n = (spot.start + spot.steps - 1) / per - first + 1;
+      if (last_arriver(a.counters + part0 + first, (unsigned)n, &lds_flag)) {
+        join_parts<D, R>(a, t, part0, first, n, wave, NW);
+        if (threadIdx.x == 0) st_cnt(a.counters + part0 + first, 0u);
+      }
+    }
+    x = spot.start + s1;
+    if (x >= end) return;
+    __syncthreads();  // LDS is free again
+    spot = find_spot(a, R, x);
   }
-}
-
-// Joins the splits of a tile, ascending: one wavefront per row, D / 64 columns a lane.
-template <int D>
-__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs a, int R) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int groups = R / 4;  // 4 rows a workgroup
-  const int head = blockIdx.x % a.w.Hkv, rest = blockIdx.x / a.w.Hkv;
-  const int slot = rest / groups, row = 4 * (rest % groups) + wave;
-  Tile t;
-  if (!tile_at(a, slot, head, R, t) || row >= t.n_rho) return;
-  const int per = steps_per_split(t.n_steps, a.S);
-  const int n = (t.n_steps + per - 1) / per;
-  if (n <= 1) return;
-  const int64_t size = (int64_t)R * (D + 2);
-  const float* part = a.part + ((int64_t)slot * a.w.Hkv + head) * a.S * size;
-  float m = -FLT_MAX;
-  for (int s = 0; s < n; ++s) m = fmaxf(m, part[s * size + R * D + row]);
-  float l = 0.0f, o[D / 64];
-#pragma unroll
-  for (int e = 0; e < D / 64; ++e) o[e] = 0.0f;
-  for (int s = 0; s < n; ++s) {
-    const float* p = part + s * size;
-    const float f = __builtin_amdgcn_exp2f(p[R * D + row] - m);
-    l += f * p[R * D + R + row];
-#pragma unroll
-    for (int e = 0; e < D / 64; ++e) o[e] += f * p[row * D + 64 * e + lane];
-  }
-  const int rho = t.rho0 + row, qi = t.s.row0 + rho / a.r, h = t.head * a.r + rho % a.r;
-  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-  uint16_t* out = a.out + (int64_t)qi * a.out_stride + (int64_t)h * D;
-#pragma unroll
-  for (int e = 0; e < D / 64; ++e)
-    out[64 * e + lane] = __builtin_bit_cast(uint16_t, (__bf16)(o[e] * inv));
-  if (a.lse && lane == 0) a.lse[(int64_t)qi * a.Hq + h] = row_lse(m, l);
 }
 
 template <int D, int FMT>
@@ -873,21 +1045,17 @@ hipError_t launch_rows(const Kv4RowsArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int D, int FMT, int NT>
-hipError_t launch_attn(const Kv4AttnArgs& a, hipStream_t st) {
-  const unsigned tiles = (unsigned)a.n_slots * a.w.Hkv;
-  kv4_attn_kernel<D, FMT, NT><<<tiles * a.S, 256, 0, st>>>(a);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.S == 1) return e;
-  kv4_join_kernel<D><<<tiles * (4 * NT), 256, 0, st>>>(a, 16 * NT);
-  return hipGetLastError();
-}
 template <int D, int FMT>
 hipError_t launch_attn(const Kv4AttnArgs& a, hipStream_t st) {
-  if (a.nt == 1) return launch_attn<D, FMT, 1>(a, st);
-  if (a.nt == 2 || D > 128) return launch_attn<D, FMT, 2>(a, st);
-  if constexpr (D <= 128) return launch_attn<D, FMT, 4>(a, st);
-  return hipErrorInvalidValue;
+  const unsigned grid = (unsigned)a.w.Hkv * (a.part ? a.n_parts : a.n_slots);
+  if constexpr (D <= 128) {
+    if (a.nt == 2) {
+      kv4_attn_rows_kernel<D, FMT, 2><<<grid, 64 * ROWS_WAVES, 0, st>>>(a);
+      return hipGetLastError();
+    }
+  }
+  kv4_attn_rows_kernel<D, FMT, 1><<<grid, 64 * ROWS_WAVES, 0, st>>>(a);
+  return hipGetLastError();
 }
 template <template <int, int> class L, class A>
 hipError_t by_type(const A& a, int D, int fmt, hipStream_t st) {

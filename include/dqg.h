@@ -400,7 +400,7 @@ int kv4_read(uint16_t* k, uint16_t* v, int T, int64_t k_stride, int64_t v_stride
 /*
  * Host only: bytes of workspace with which kv4_attention splits long caches over workgroups, for
  * up to T rows of B sequences of up to max_kv_len positions (0: such calls never split).  0 also
- * for invalid sizes.  Grows with T, B and max_kv_len.
+ * for invalid sizes.  Never shrinks as T, B or max_kv_len grow.
  */
 size_t kv4_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int max_kv_len);
 
@@ -417,9 +417,10 @@ size_t kv4_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int m
  *   lse      fp32 [T, Hq] or NULL
  *   max_rows, max_kv_len: no sequence has more rows or positions than these (0: not known).
  *            They choose the launch shape only; the result is right for any value.
- *   workspace NULL (no splits: correct, slower where few rows meet a long cache), or at least
- *            kv4_attention_workspace_bytes(T, B, Hq, Hkv, D, max_kv_len, or max_pages *
- *            page_size where that is 0).  Scratch: no contents are expected or kept.
+ *   workspace NULL (a cache is not split over workgroups: correct, slower where few rows meet a
+ *            long one), or at least kv4_attention_workspace_bytes(T, B, Hq, Hkv, D, max_kv_len, or
+ *            max_pages * page_size where that is 0), zero-filled before its first use; every
+ *            completed call leaves it ready for the next, of any sizes that it suffices for.
  * Products on fp16 matrix cores with fp32 sums.  Cached values enter exactly for scales from
  * 2^-17 on (below, within 2^-25 of the value per code step) and must stay below 16384 (INT4) or
  * 65504 (FP4) in magnitude; |q| < 65504, and |q| < 2^-14 enters within 2^-25.  Softmax

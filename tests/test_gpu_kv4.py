@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import kv4_util as U
-from gpu_util import bits16, bf16_f64, dev, guarded
+from gpu_util import bits16, bf16_f64, dev, guarded, guarded_workspace
 from oracle import kv4_oracle as K
 
 pytestmark = pytest.mark.gpu
@@ -204,7 +204,7 @@ def run_attention(c, q, cu, lens, table, fmt, G, page, scale=None, window=0, sin
     if split:
         need = B.kv4_attention_workspace_bytes(T, len(lens), Hq, c.H, D, table.shape[1] * page)
         if need:
-            ws, check_ws = guarded((need,), torch.uint8)
+            ws, check_ws = guarded_workspace(need)
     kw = {}
     if hints:
         kw = dict(max_rows=int(np.diff(cu).max()), max_kv_len=max(int(lens.max()), 1))
