@@ -303,11 +303,10 @@ bool gemv_sizes_ok(int T, int K, int N, int group) {
 constexpr int kKv4MaxT = 1 << 22;
 constexpr int kKv4MaxB = 65536;
 constexpr int kKv4MaxHeads = 1024;
-// Workgroups of the attention kernel that run at once (256 compute units; two of 8 wavefronts
-// each where a workgroup holds 16 rows of up to 128, else one): the line of steps is cut into as
-// many parts.
-constexpr int kKv4Resident = 512;
-constexpr int kKv4MinSteps = 8;  // steps of a part, at least: one for each wavefront
+// Workgroups of the attention kernel that run at once, one of 8 wavefronts a compute unit: the line
+// of steps is cut into as many parts.
+constexpr int kKv4Resident = 256;
+constexpr int kKv4MinSteps = 32;  // steps of a part, at least
 
 inline bool kv4_heads_ok(int Hkv, int D) {
   return Hkv >= 1 && Hkv <= kKv4MaxHeads && (D == 64 || D == 128 || D == 256);
@@ -322,22 +321,25 @@ struct Kv4Plan {
   int nt, slots, parts;
 };
 // parts of a head's steps: as many as run at once
-int kv4_parts(int Hkv, int D, int nt) {
-  const int wgs = nt == 1 && D <= 128 ? kKv4Resident : kKv4Resident / 2;
-  return std::max(wgs / Hkv, 1);
-}
-Kv4Plan plan_kv4(int T, int B, int Hq, int Hkv, int D, int rows) {
+int kv4_parts(int Hkv) { return std::max(kKv4Resident / Hkv, 1); }
+Kv4Plan plan_kv4(int T, int B, int Hq, int Hkv, int D, int rows, long long steps) {
   const int r = Hq / Hkv;
   Kv4Plan p{};
   rows = std::max(std::min(rows, T), (T + B - 1) / B);
   // one 16-row tile holds a token's heads; more rows share the decoded keys and values
   p.nt = (long long)rows * r <= 16 || D > 128 ? 1 : 2;
-  p.slots = (int)((long long)T * r / (16 * p.nt)) + B;
-  p.parts = kv4_parts(Hkv, D, p.nt);
+  const int R = 16 * p.nt;
+  p.slots = (int)((long long)T * r / R) + B;
+  const long long tiles = std::min<long long>(p.slots, (long long)B * (((long long)rows * r + R - 1) / R));
+  p.parts = (int)std::max(1LL, std::min<long long>(kv4_parts(Hkv), (tiles * steps + kKv4MinSteps - 1) /
+                                                                       kKv4MinSteps));
   return p;
 }
 // [counters, one a part][partials, two a part]
 size_t kv4_counter_bytes() { return sizeof(unsigned) * std::max(kKv4Resident, kKv4MaxHeads); }
+long long kv4_steps(long long positions) {
+  return (positions + dqg::KV4_STEP - 1) / dqg::KV4_STEP;
+}
 bool kv4_attn_sizes_ok(int T, int B, int Hq, int Hkv, int D) {
   return T >= 1 && T <= kKv4MaxT && B >= 1 && B <= kKv4MaxB && kv4_heads_ok(Hkv, D) && Hq >= 1 &&
          Hq % Hkv == 0 && Hq <= 65536 && (long long)T * Hq < (1LL << 30);
@@ -718,11 +720,8 @@ int kv4_read(uint16_t* k, uint16_t* v, int T, int64_t k_stride, int64_t v_stride
 size_t kv4_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int max_kv_len) {
   if (!kv4_attn_sizes_ok(T, B, Hq, Hkv, D) || max_kv_len < 1 || max_kv_len > (1 << 30)) return 0;
   if (max_kv_len <= kKv4MinSteps * dqg::KV4_STEP) return 0;
-  size_t most = 0;
-  for (int nt = 1; nt <= (D > 128 ? 1 : 2); ++nt)
-    most = std::max(most, 2 * (size_t)Hkv * kv4_parts(Hkv, D, nt) * sizeof(float) *
-                              dqg::kv4_part_floats(nt, D));
-  return up256(kv4_counter_bytes() + most);
+  return up256(kv4_counter_bytes() + 2 * (size_t)Hkv * kv4_parts(Hkv) * sizeof(float) *
+                                         dqg::kv4_part_floats(D > 128 ? 1 : 2, D));
 }
 
 int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32_t* cu_rows,
@@ -747,12 +746,17 @@ int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32
   const int most = max_kv_len ? std::min(max_kv_len, cap) : cap;
   if (workspace && workspace_bytes < kv4_attention_workspace_bytes(T, B, Hq, Hkv, D, most))
     return DQG_ERR_WORKSPACE;
-  const Kv4Plan p = plan_kv4(T, B, Hq, Hkv, D, max_rows ? max_rows : T);
+  long long steps = kv4_steps(most);
+  if (window > 0)  // a tile of up to 32 rows sees `window` positions a row and the first ones
+    steps = std::min(steps, kv4_steps((long long)window + 32) + 1 + kv4_steps(sinks));
+  const Kv4Plan p = plan_kv4(T, B, Hq, Hkv, D, max_rows ? max_rows : T, steps);
   dqg::Kv4AttnArgs a{};
   a.w = kv4_where(T, B, cu_rows, kv_lens, block_table, max_pages, cache, num_pages, Hkv, D,
                   page_size, group, status);
   a.q = q; a.q_stride = q_stride; a.out = out; a.out_stride = out_stride; a.lse = lse;
   a.Hq = Hq; a.r = Hq / Hkv; a.scale = scale; a.window = window; a.sinks = sinks;
+  a.r_shift = a.r > 1 ? 32 - __builtin_clz((unsigned)(a.r - 1)) : 0;
+  a.r_mul = (uint32_t)(((1ull << 32) * ((1ull << a.r_shift) - a.r)) / a.r + 1);
   a.n_slots = p.slots; a.nt = p.nt; a.n_parts = p.parts; a.min_steps = kKv4MinSteps;
   // (places on the line are 32-bit)
   if (workspace && (long long)p.slots * (cap / dqg::KV4_STEP) < (1LL << 30)) {

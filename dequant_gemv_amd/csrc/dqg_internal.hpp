@@ -153,6 +153,8 @@ struct Kv4AttnArgs {
   float* part;           // partial sums, two a part and head; null: tiles are not cut
   unsigned* counters;    // [Hkv * n_parts], zero between calls
   int Hq, r;             // query heads, and query heads per kv head
+  uint32_t r_mul;        // division by r (see row_of)
+  int r_shift;
   float scale;
   int window, sinks;
   int n_slots, n_parts;  // row-tile slots; parts of a head's steps

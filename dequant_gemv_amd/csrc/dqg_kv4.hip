@@ -407,18 +407,22 @@ struct Tile {
   int p_lo, p_hi;            // positions of the first and last row
   int n_steps, sink_steps, main0;  // steps 0 .. sink_steps - 1, then main0, main0 + 1, ...
 };
-__device__ __forceinline__ bool tile_of(const Kv4AttnArgs& a, int b, int j, int head, int R,
-                                        Tile& t) {
+// rho / r for 0 <= rho < 2^30: r_mul = floor(2^32 (2^s - r) / r) + 1, s = ceil(log2 r)
+__device__ __forceinline__ int row_of(const Kv4AttnArgs& a, int rho) {
+  return (int)((__umulhi((uint32_t)rho, a.r_mul) + (uint32_t)rho) >> a.r_shift);
+}
+__device__ __forceinline__ bool tile_of(const Kv4AttnArgs& a, const Seq& s, int b, int j, int head,
+                                        int R, Tile& t) {
   const int r = a.r;
   t.b = b;
-  t.s = seq_at(a.w, b);
+  t.s = s;
   t.head = head;
   t.rho0 = j * R;
   t.n_rho = min(R, t.s.n * r - t.rho0);
   if (j < 0 || t.n_rho <= 0) return false;
   const int first = t.s.len - t.s.n;
-  t.p_lo = first + t.rho0 / r;
-  t.p_hi = first + (t.rho0 + t.n_rho - 1) / r;
+  t.p_lo = first + row_of(a, t.rho0);
+  t.p_hi = first + row_of(a, t.rho0 + t.n_rho - 1);
   const int end = min(t.p_hi + 1, t.s.cap);  // positions beyond the table hold nothing
   t.n_steps = t.sink_steps = t.main0 = 0;
   if (end > 0) {
@@ -439,8 +443,8 @@ __device__ __forceinline__ int position_of(const Tile& t, int step) {
 __device__ __forceinline__ bool tile_at(const Kv4AttnArgs& a, int slot, int head, int R, Tile& t) {
   const int r = a.r;
   const int b = seq_of_slot(a.w, slot, 1, [=](int c) { return (int)((int64_t)c * r / R); });
-  const int row0 = min(max(a.w.cu[b], 0), a.w.T);
-  return tile_of(a, b, slot - ((int)((int64_t)row0 * r / R) + b), head, R, t);
+  const Seq s = seq_at(a.w, b);
+  return tile_of(a, s, b, slot - ((int)((int64_t)s.row0 * r / R) + b), head, R, t);
 }
 
 template <int D>
@@ -556,29 +560,37 @@ struct Queries {
   f16x8_t q[NT][D / 32];
   int pos[NT];
 };
-template <int D, int FMT, int NT>
+template <int D, int NT>
 __device__ __forceinline__ void load_queries(const Kv4AttnArgs& a, const Tile& t, int q16, int g,
-                                             Queries<D, NT>& x) {
+                                             uint4 (&u)[NT][D / 32], int (&pos)[NT]) {
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int rho = t.rho0 + 16 * nt + q16;
     const bool on = 16 * nt + q16 < t.n_rho;
-    const int i = rho / a.r, h = t.head * a.r + rho % a.r;
-    x.pos[nt] = on ? t.s.len - t.s.n + i : -1;
+    const int i = row_of(a, rho), h = t.head * a.r + rho - i * a.r;
+    pos[nt] = on ? t.s.len - t.s.n + i : -1;
     const uint16_t* p = a.q + (int64_t)(t.s.row0 + i) * a.q_stride + (int64_t)h * D;
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
       const int d0 = D == 64 ? 16 * g + 8 * j : 128 * (j / 4) + 32 * g + 8 * (j % 4);
-      uint4 u = make_uint4(0, 0, 0, 0);
-      if (on) u = *reinterpret_cast<const uint4*>(p + d0);
-      const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+      u[nt][j] = make_uint4(0, 0, 0, 0);
+      if (on) u[nt][j] = *reinterpret_cast<const uint4*>(p + d0);
+    }
+  }
+}
+template <int D, int FMT, int NT>
+__device__ __forceinline__ void convert_queries(const uint4 (&u)[NT][D / 32], Queries<D, NT>& x) {
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      const uint32_t uw[4] = {u[nt][j].x, u[nt][j].y, u[nt][j].z, u[nt][j].w};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int d = value_at<FMT>(e);
         x.q[nt][j][e] = (_Float16)((d & 1) ? bf16_hi(uw[d / 2]) : bf16_lo(uw[d / 2]));
       }
     }
-  }
 }
 
 template <int D, int NT>
@@ -762,33 +774,58 @@ __device__ __forceinline__ void seq_work(const Kv4AttnArgs& a, const Seq& s, int
   }
   *steps = max(w, 1);
 }
-struct Spot {  // a place on the line
-  int b, tile, steps;  // sequence, its tile, steps of each of its tiles
-  int start;           // where the tile starts
+// 64 sequences of the line, one a lane: where they are on it and what they hold.
+struct Chunk {
+  int b0, incl, mine, steps;  // incl: places of the chunk up to and with this sequence's
+  Seq s;
 };
-// The tile that holds place x (x < total), or with x < 0 the line's length in start.
-__device__ __forceinline__ Spot find_spot(const Kv4AttnArgs& a, int R, int x) {
-  const int lane = threadIdx.x & 63;
-  Spot f{0, 0, 1, 0};
-  int before = 0;
-  for (int b0 = 0; b0 < a.w.B; b0 += 64) {
-    int tiles = 0, steps = 1;
-    if (b0 + lane < a.w.B) seq_work(a, seq_at(a.w, b0 + lane), R, &tiles, &steps);
-    const int mine = tiles * steps;
-    const int incl = wave_incl_sum(mine);
-    const int all = __builtin_amdgcn_readlane(incl, 63);
-    if (x >= 0 && x < before + all) {
-      const int i = __popcll(__ballot(before + incl <= x));
-      const int s0 = before + __builtin_amdgcn_readlane(incl - mine, i);
-      f.b = b0 + i;
-      f.steps = __builtin_amdgcn_readlane(steps, i);
-      f.tile = (x - s0) / f.steps;
-      f.start = s0 + f.tile * f.steps;
-      return f;
-    }
-    before += all;
+__device__ __forceinline__ void load_chunk(const Kv4AttnArgs& a, int R, int b0, Chunk& c) {
+  const int b = b0 + (threadIdx.x & 63);
+  int tiles = 0;
+  c.b0 = b0;
+  c.steps = 1;
+  c.s = Seq{0, 0, 0, 0};
+  if (b < a.w.B) {
+    c.s = seq_at(a.w, b);
+    seq_work(a, c.s, R, &tiles, &c.steps);
   }
-  f.start = before;
+  c.mine = tiles * c.steps;
+  c.incl = wave_incl_sum(c.mine);
+}
+// The line's length; c: its first chunk.
+__device__ __forceinline__ int line_length(const Kv4AttnArgs& a, int R, Chunk& c) {
+  int n = 0;
+  for (int b0 = (a.w.B - 1) & ~63; b0 >= 0; b0 -= 64) {
+    load_chunk(a, R, b0, c);
+    n += __builtin_amdgcn_readlane(c.incl, 63);
+  }
+  return n;
+}
+struct Spot {  // a tile on the line
+  int b, tile, steps, start;  // sequence, its tile, the tile's places and the first of them
+  Seq s;
+};
+// The tile that holds place x; c: the line's first chunk (read again where it does not hold x).
+__device__ __forceinline__ Spot find_spot(const Kv4AttnArgs& a, int R, int x, Chunk& c) {
+  int before = 0;
+  while (true) {
+    const int all = __builtin_amdgcn_readlane(c.incl, 63);
+    if (x < before + all || c.b0 + 64 >= a.w.B) break;
+    before += all;
+    load_chunk(a, R, c.b0 + 64, c);
+  }
+  const int i = min(__popcll(__ballot(before + c.incl <= x)), 63);
+  Spot f;
+  f.b = c.b0 + i;
+  f.steps = __builtin_amdgcn_readlane(c.steps, i);
+  const int s0 = before + __builtin_amdgcn_readlane(c.incl - c.mine, i);
+  f.tile = (x - s0) / f.steps;
+  f.start = s0 + f.tile * f.steps;
+  f.s.row0 = __builtin_amdgcn_readlane(c.s.row0, i);
+  f.s.n = __builtin_amdgcn_readlane(c.s.n, i);
+  f.s.len = __builtin_amdgcn_readlane(c.s.len, i);
+  f.s.cap = __builtin_amdgcn_readlane(c.s.cap, i);
+  if (c.b0 > 0) load_chunk(a, R, 0, c);
   return f;
 }
 
@@ -810,7 +847,8 @@ __device__ __forceinline__ float4 ld4_agent(__amdgpu_buffer_rsrc_t r, int word) 
 // Output of 4 columns of one row.
 __device__ __forceinline__ void store_out4(const Kv4AttnArgs& a, const Tile& t, int D, int row, int d,
                                            float4 v, float inv) {
-  const int rho = t.rho0 + row, qi = t.s.row0 + rho / a.r, h = t.head * a.r + rho % a.r;
+  const int rho = t.rho0 + row, i = row_of(a, rho), qi = t.s.row0 + i;
+  const int h = t.head * a.r + rho - i * a.r;
   const bf16x2_t lo = {(__bf16)(v.x * inv), (__bf16)(v.y * inv)};
   const bf16x2_t hi = {(__bf16)(v.z * inv), (__bf16)(v.w * inv)};
   *reinterpret_cast<uint2*>(a.out + (int64_t)qi * a.out_stride + (int64_t)h * D + d) =
@@ -818,7 +856,8 @@ __device__ __forceinline__ void store_out4(const Kv4AttnArgs& a, const Tile& t, 
 }
 __device__ __forceinline__ void store_lse(const Kv4AttnArgs& a, const Tile& t, int row, float m,
                                           float l) {
-  const int rho = t.rho0 + row, qi = t.s.row0 + rho / a.r, h = t.head * a.r + rho % a.r;
+  const int rho = t.rho0 + row, i = row_of(a, rho), qi = t.s.row0 + i;
+  const int h = t.head * a.r + rho - i * a.r;
   if (a.lse) a.lse[(int64_t)qi * a.Hq + h] = row_lse(m, l);
 }
 
@@ -835,31 +874,42 @@ __device__ __forceinline__ void join_parts(const Kv4AttnArgs& a, const Tile& t, 
     float m = -FLT_MAX, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int k0 = 0; k0 < n; k0 += 64) {
-      const int k = k0 + lane;
-      float pm = -FLT_MAX, pl = 0.0f;
-      if (k < n) {
-        const int at = (2 * (part0 + first + k) + (k == 0)) * SIZE + R * D + row;
-        pm = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at * 4, 0, 16));
-        pl = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (at + R) * 4, 0, 16));
-      }
-      float mx = pm;
-#pragma unroll
-      for (int i = 1; i < 64; i *= 2) mx = fmaxf(mx, __shfl_xor(mx, i));
-      mx = fmaxf(mx, m);
-      const float f0 = __builtin_amdgcn_exp2f(m - mx);
-      m = mx;
-      const float f = __builtin_amdgcn_exp2f(pm - m);
-      l = l * f0 + f * pl;
-      o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
+      const int k = min(k0 + lane, n - 1);
       const int here = min(n - k0, 64);
-#pragma unroll 8
-      for (int j = 0; j < here; j += PL) {
-        const int kk = min(j + sub, here - 1);
-        const float4 v = ld4_agent(r, (2 * (part0 + first + k0 + kk) + (k0 + kk == 0)) * SIZE +
-                                          row * D + d);
-        float fk = __shfl(f, kk);  // (every lane takes part)
-        fk = j + sub < here ? fk : 0.0f;
-        o.x += fk * v.x; o.y += fk * v.y; o.z += fk * v.z; o.w += fk * v.w;
+      const int at = (2 * (part0 + first + k) + (k == 0)) * SIZE + R * D + row;
+      float pm = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at * 4, 0, 16));
+      float pl = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (at + R) * 4, 0, 16));
+      float f = 0.0f;
+      constexpr int UN = 16;  // loads in flight
+      for (int j0 = 0; j0 < here; j0 += UN * PL) {
+        float4 v[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+          const int kk = k0 + min(j0 + u * PL + sub, here - 1);
+          v[u] = ld4_agent(r, (2 * (part0 + first + kk) + (kk == 0)) * SIZE + row * D + d);
+        }
+        if (j0 == 0) {  // the chunk's weights, while the first sums are on their way
+          if (lane >= here) {
+            pm = -FLT_MAX;
+            pl = 0.0f;
+          }
+          float mx = pm;
+#pragma unroll
+          for (int i = 1; i < 64; i *= 2) mx = fmaxf(mx, __shfl_xor(mx, i));
+          mx = fmaxf(mx, m);
+          const float f0 = __builtin_amdgcn_exp2f(m - mx);
+          m = mx;
+          f = __builtin_amdgcn_exp2f(pm - m);
+          l = l * f0 + f * pl;
+          o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
+        }
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+          const int j = j0 + u * PL + sub;
+          float fk = __shfl(f, min(j, here - 1));  // (every lane takes part)
+          fk = j < here ? fk : 0.0f;
+          o.x += fk * v[u].x; o.y += fk * v[u].y; o.z += fk * v[u].z; o.w += fk * v[u].w;
+        }
       }
     }
 #pragma unroll
@@ -874,9 +924,12 @@ __device__ __forceinline__ void join_parts(const Kv4AttnArgs& a, const Tile& t, 
   }
 }
 
+// The step's K and V (PREFETCH: and the next step's) are in registers: 8 wavefronts a compute unit
+// keep 37 or 74 KB in flight.
 template <int D, int FMT, int NT>
-__global__ __launch_bounds__(64 * ROWS_WAVES, NT == 1 && D <= 128 ? 4 : 2) void kv4_attn_rows_kernel(Kv4AttnArgs a) {
+__global__ __launch_bounds__(64 * ROWS_WAVES, 2) void kv4_attn_rows_kernel(Kv4AttnArgs a) {
   constexpr int R = 16 * NT, LD = D + 4, NW = ROWS_WAVES, SIZE = R * (D + 2);
+  constexpr bool PREFETCH = D * NT <= 128;
   __shared__ float lds_o[NW][16][LD];
   __shared__ float lds_m[NW][R], lds_l[NW][R];
   __shared__ int lds_flag;
@@ -885,16 +938,16 @@ __global__ __launch_bounds__(64 * ROWS_WAVES, NT == 1 && D <= 128 ? 4 : 2) void 
   const int head = blockIdx.x % a.w.Hkv, part = blockIdx.x / a.w.Hkv;
   const int part0 = head * a.n_parts;
   const bool cut = a.part != nullptr;  // without partials a part is a whole tile
-  int x, end, per = 1;
+  int x = 0, end = 0, per = 1;
   Spot spot;
+  Chunk chunk;
   if (cut) {
-    const int total = find_spot(a, R, -1).start;
+    const int total = line_length(a, R, chunk);
     per = max((total + a.n_parts - 1) / a.n_parts, a.min_steps);
     per = (per + NW - 1) / NW * NW;  // a shorter part takes a wavefront as long
     x = part * per;
     end = min(x + per, total);
     if (x >= end) return;
-    spot = find_spot(a, R, x);
   }
   Tile t;
   const float c = a.scale * LOG2E;
@@ -903,7 +956,8 @@ __global__ __launch_bounds__(64 * ROWS_WAVES, NT == 1 && D <= 128 ? 4 : 2) void 
     int s0 = 0, s1;
     bool whole = true;
     if (cut) {
-      tile_of(a, spot.b, spot.tile, head, R, t);
+      spot = find_spot(a, R, x, chunk);
+      tile_of(a, spot.s, spot.b, spot.tile, head, R, t);
       s0 = x - spot.start;
       s1 = min(end - spot.start, spot.steps);
       whole = s0 == 0 && s1 == spot.steps;
@@ -912,47 +966,60 @@ __global__ __launch_bounds__(64 * ROWS_WAVES, NT == 1 && D <= 128 ? 4 : 2) void 
       s1 = t.n_steps;
     }
     if (t.s.len > t.s.cap && s0 == 0 && threadIdx.x == 0) report(a.w.status, ST_LENGTH);
-    Queries<D, NT> q;
-    load_queries<D, FMT, NT>(a, t, q16, g, q);
     Acc<D, NT> acc;
     acc.clear();
     bool all_ok = true;
     const int last = min(s1, t.n_steps);
+    uint4 raw[NT][D / 32];
+    Queries<D, NT> q;
+    bool first_round = true;
     for (int base = s0 + wave; base < last; base += 64 * NW) {
       // pages of up to 64 of the wavefront's steps, one a lane; -1: no such page
       int pages;
       {
         const int step = min(base + lane * NW, last - 1);
         pages = a.w.table[(int64_t)t.b * a.w.max_pages + (position_of(t, step) >> a.w.page_shift)];
-        if (pages < 0 || pages >= a.w.num_pages) pages = -1;
       }
+      if (first_round) load_queries<D, NT>(a, t, q16, g, raw, q.pos);
+      if (pages < 0 || pages >= a.w.num_pages) pages = -1;
       const int n = min((last - base + NW - 1) / NW, 64);
-      KStage<D> ks;
-      VStage<D> vs;
-      int t0 = position_of(t, base);
-      int page = __builtin_amdgcn_readlane(pages, 0);
-      Place pl = place_of<D>(a.w, head, max(page, 0), t0);
-      load_k<D>(pl, off, ks);
-      load_v<D>(pl, off, vs);
-      for (int i = 0; i < n; ++i) {
-        const bool more = i + 1 < n;
-        const int t0n = position_of(t, min(base + (i + 1) * NW, last - 1));
-        const int pagen = __builtin_amdgcn_readlane(pages, min(i + 1, n - 1));
-        const Place pln = place_of<D>(a.w, head, max(pagen, 0), t0n);
-        f32x4_t sc[NT][2];
-        step_scores<D, FMT, NT>(ks, q, c, sc);
-        if (more) load_k<D>(pln, off, ks);
-        if (page >= 0) {
-          if (step_at_edge(a, t, t0)) step_mask<D, NT>(a, t, t0, g, q, sc, vs.s);
-          f16x8_t p[NT];
-          step_weights<D, FMT, NT>(sc, acc, p);
-          step_values<D, FMT, NT>(vs, p, acc);
-        } else {
+      KStage<D> k0, k1;
+      VStage<D> v0, v1;
+      const auto load = [&](int i, KStage<D>& k, VStage<D>& v) {
+        const int page = __builtin_amdgcn_readlane(pages, i);
+        const Place pl = place_of<D>(a.w, head, max(page, 0), position_of(t, base + i * NW));
+        load_k<D>(pl, off, k);
+        load_v<D>(pl, off, v);
+      };
+      const auto compute = [&](int i, KStage<D>& k, VStage<D>& v) {
+        if (__builtin_amdgcn_readlane(pages, i) < 0) {
           all_ok = false;
+          return;
         }
-        if (more) load_v<D>(pln, off, vs);
-        t0 = t0n;
-        page = pagen;
+        const int t0 = position_of(t, base + i * NW);
+        f32x4_t sc[NT][2];
+        step_scores<D, FMT, NT>(k, q, c, sc);
+        if (step_at_edge(a, t, t0)) step_mask<D, NT>(a, t, t0, g, q, sc, v.s);
+        f16x8_t p[NT];
+        step_weights<D, FMT, NT>(sc, acc, p);
+        step_values<D, FMT, NT>(v, p, acc);
+      };
+      load(0, k0, v0);
+      if (first_round) convert_queries<D, FMT, NT>(raw, q);
+      first_round = false;
+      if constexpr (PREFETCH) {
+        for (int i = 0; i < n; i += 2) {
+          if (i + 1 < n) load(i + 1, k1, v1);
+          compute(i, k0, v0);
+          if (i + 1 >= n) break;
+          if (i + 2 < n) load(i + 2, k0, v0);
+          compute(i + 1, k1, v1);
+        }
+      } else {
+        for (int i = 0; i < n; ++i) {
+          compute(i, k0, v0);
+          if (i + 1 < n) load(i + 1, k0, v0);
+        }
       }
     }
     if (!all_ok && lane == 0) report(a.w.status, ST_PAGE);
@@ -1030,7 +1097,6 @@ __global__ __launch_bounds__(64 * ROWS_WAVES, NT == 1 && D <= 128 ? 4 : 2) void 
     x = spot.start + s1;
     if (x >= end) return;
     __syncthreads();  // LDS is free again
-    spot = find_spot(a, R, x);
   }
 }
 
