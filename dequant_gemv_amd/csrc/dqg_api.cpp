@@ -306,7 +306,11 @@ constexpr int kKv4MaxHeads = 1024;
 // Workgroups of the attention kernel that run at once, one of 8 wavefronts a compute unit: the line
 // of steps is cut into as many parts.
 constexpr int kKv4Resident = 256;
-constexpr int kKv4MinSteps = 32;  // steps of a part, at least
+constexpr int kKv4MinSteps = 8;       // steps of a part, at least: one for each wavefront
+constexpr int kKv4MinTileSteps = 32;  // the same of the kernel for many rows
+// rows (query rows times the query heads of a kv head) of a sequence from which on it goes to the
+// kernel for many rows
+constexpr int kKv4FewRows = 32;
 
 inline bool kv4_heads_ok(int Hkv, int D) {
   return Hkv >= 1 && Hkv <= kKv4MaxHeads && (D == 64 || D == 128 || D == 256);
@@ -317,24 +321,8 @@ inline bool kv4_page_ok(int D, int page_size, int group) {
 }
 inline int log2_of(int v) { return 31 - __builtin_clz((unsigned)v); }
 
-struct Kv4Plan {
-  int nt, slots, parts;
-};
 // parts of a head's steps: as many as run at once
 int kv4_parts(int Hkv) { return std::max(kKv4Resident / Hkv, 1); }
-Kv4Plan plan_kv4(int T, int B, int Hq, int Hkv, int D, int rows, long long steps) {
-  const int r = Hq / Hkv;
-  Kv4Plan p{};
-  rows = std::max(std::min(rows, T), (T + B - 1) / B);
-  // one 16-row tile holds a token's heads; more rows share the decoded keys and values
-  p.nt = (long long)rows * r <= 16 || D > 128 ? 1 : 2;
-  const int R = 16 * p.nt;
-  p.slots = (int)((long long)T * r / R) + B;
-  const long long tiles = std::min<long long>(p.slots, (long long)B * (((long long)rows * r + R - 1) / R));
-  p.parts = (int)std::max(1LL, std::min<long long>(kv4_parts(Hkv), (tiles * steps + kKv4MinSteps - 1) /
-                                                                       kKv4MinSteps));
-  return p;
-}
 // [counters, one a part][partials, two a part]
 size_t kv4_counter_bytes() { return sizeof(unsigned) * std::max(kKv4Resident, kKv4MaxHeads); }
 long long kv4_steps(long long positions) {
@@ -721,7 +709,7 @@ size_t kv4_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int m
   if (!kv4_attn_sizes_ok(T, B, Hq, Hkv, D) || max_kv_len < 1 || max_kv_len > (1 << 30)) return 0;
   if (max_kv_len <= kKv4MinSteps * dqg::KV4_STEP) return 0;
   return up256(kv4_counter_bytes() + 2 * (size_t)Hkv * kv4_parts(Hkv) * sizeof(float) *
-                                         dqg::kv4_part_floats(D > 128 ? 1 : 2, D));
+                                         dqg::kv4_part_floats(dqg::KV4_TILE_NT, D));
 }
 
 int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32_t* cu_rows,
@@ -747,9 +735,8 @@ int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32
   if (workspace && workspace_bytes < kv4_attention_workspace_bytes(T, B, Hq, Hkv, D, most))
     return DQG_ERR_WORKSPACE;
   long long steps = kv4_steps(most);
-  if (window > 0)  // a tile of up to 32 rows sees `window` positions a row and the first ones
-    steps = std::min(steps, kv4_steps((long long)window + 32) + 1 + kv4_steps(sinks));
-  const Kv4Plan p = plan_kv4(T, B, Hq, Hkv, D, max_rows ? max_rows : T, steps);
+  if (window > 0)  // a tile of up to 256 rows sees `window` positions a row and the first ones
+    steps = std::min(steps, kv4_steps((long long)window + 256) + 1 + kv4_steps(sinks));
   dqg::Kv4AttnArgs a{};
   a.w = kv4_where(T, B, cu_rows, kv_lens, block_table, max_pages, cache, num_pages, Hkv, D,
                   page_size, group, status);
@@ -757,15 +744,37 @@ int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32
   a.Hq = Hq; a.r = Hq / Hkv; a.scale = scale; a.window = window; a.sinks = sinks;
   a.r_shift = a.r > 1 ? 32 - __builtin_clz((unsigned)(a.r - 1)) : 0;
   a.r_mul = (uint32_t)(((1ull << 32) * ((1ull << a.r_shift) - a.r)) / a.r + 1);
-  a.n_slots = p.slots; a.nt = p.nt; a.n_parts = p.parts; a.min_steps = kKv4MinSteps;
-  // (places on the line are 32-bit)
-  if (workspace && (long long)p.slots * (cap / dqg::KV4_STEP) < (1LL << 30)) {
-    a.counters = static_cast<unsigned*>(workspace);
-    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kv4_counter_bytes());
-  } else if ((long long)p.slots * Hkv >= (1LL << 31)) {
-    return DQG_ERR_UNSUPPORTED;
+  const int rows = std::max(std::min(max_rows ? max_rows : T, T), (T + B - 1) / B);
+  const int few = kKv4FewRows / a.r;  // rows of a sequence that are few
+  const auto launch = [&](int nt, int over, int to, int min_steps) -> int {
+    const int R = 16 * nt;
+    a.nt = nt;
+    a.rows_over = over;
+    a.rows_to = to;
+    a.min_steps = min_steps;
+    a.n_slots = (int)((long long)T * a.r / R) + B;
+    const long long tiles =
+        Hkv * std::min<long long>(a.n_slots, (long long)B * (((long long)rows * a.r + R - 1) / R));
+    a.n_parts = (int)std::max(1LL, std::min<long long>(kv4_parts(Hkv), (tiles / Hkv * steps + min_steps - 1) /
+                                                                           min_steps));
+    // many-row tiles are cut only where they are too few to fill the GPU by themselves (two rounds);
+    // places on the line are 32-bit
+    const bool cut = workspace && (nt < dqg::KV4_TILE_NT || tiles < 2 * kKv4Resident) &&
+                     (long long)a.n_slots * (cap / dqg::KV4_STEP) < (1LL << 30);
+    a.counters = cut ? static_cast<unsigned*>(workspace) : nullptr;
+    a.part = cut ? reinterpret_cast<float*>(static_cast<char*>(workspace) + kv4_counter_bytes())
+                 : nullptr;
+    if ((long long)a.n_slots * Hkv >= (1LL << 31)) return DQG_ERR_UNSUPPORTED;
+    return dqg::launch_kv4_attention(a, D, format, stream) == hipSuccess ? DQG_OK : DQG_ERR_HIP;
+  };
+  // one 16-row tile holds a token's heads; two share the decoded keys and values
+  const int nt = (long long)rows * a.r <= 16 || D > 128 ? 1 : 2;
+  if (rows <= few) return launch(nt, 0, INT_MAX, kKv4MinSteps);
+  if (B > 1 && few > 0) {  // sequences of few rows among those of many
+    rc = launch(nt, 0, few, kKv4MinSteps);
+    if (rc != DQG_OK) return rc;
   }
-  return dqg::launch_kv4_attention(a, D, format, stream) == hipSuccess ? DQG_OK : DQG_ERR_HIP;
+  return launch(dqg::KV4_TILE_NT, B > 1 ? few : 0, INT_MAX, kKv4MinTileSteps);
 }
 
 int packed_dequant_f32(const uint8_t* w, const uint16_t* s, int K, int N, int group,

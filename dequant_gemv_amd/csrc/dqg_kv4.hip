@@ -435,6 +435,10 @@ __device__ __forceinline__ bool tile_of(const Kv4AttnArgs& a, const Seq& s, int 
   }
   return true;
 }
+// Whether the launch is the one that takes this sequence (a call of few and many rows has two).
+__device__ __forceinline__ bool takes_seq(const Kv4AttnArgs& a, const Seq& s) {
+  return s.n > a.rows_over && s.n <= a.rows_to;
+}
 __device__ __forceinline__ int position_of(const Tile& t, int step) {
   return (step < t.sink_steps ? step : step - t.sink_steps + t.main0) * KV4_STEP;
 }
@@ -444,7 +448,7 @@ __device__ __forceinline__ bool tile_at(const Kv4AttnArgs& a, int slot, int head
   const int r = a.r;
   const int b = seq_of_slot(a.w, slot, 1, [=](int c) { return (int)((int64_t)c * r / R); });
   const Seq s = seq_at(a.w, b);
-  return tile_of(a, s, b, slot - ((int)((int64_t)s.row0 * r / R) + b), head, R, t);
+  return takes_seq(a, s) && tile_of(a, s, b, slot - ((int)((int64_t)s.row0 * r / R) + b), head, R, t);
 }
 
 template <int D>
@@ -763,7 +767,7 @@ constexpr int ROWS_WAVES = 8;
 // one step, so that its rows are written.
 __device__ __forceinline__ void seq_work(const Kv4AttnArgs& a, const Seq& s, int R, int* tiles,
                                          int* steps) {
-  *tiles = (int)(((int64_t)s.n * a.r + R - 1) / R);
+  *tiles = takes_seq(a, s) ? (int)(((int64_t)s.n * a.r + R - 1) / R) : 0;
   const int end = min(s.len, s.cap);
   int w = (end + KV4_STEP - 1) / KV4_STEP;
   if (a.window > 0) {
@@ -924,12 +928,9 @@ __device__ __forceinline__ void join_parts(const Kv4AttnArgs& a, const Tile& t, 
   }
 }
 
-// The step's K and V (PREFETCH: and the next step's) are in registers: 8 wavefronts a compute unit
-// keep 37 or 74 KB in flight.
 template <int D, int FMT, int NT>
 __global__ __launch_bounds__(64 * ROWS_WAVES, 2) void kv4_attn_rows_kernel(Kv4AttnArgs a) {
   constexpr int R = 16 * NT, LD = D + 4, NW = ROWS_WAVES, SIZE = R * (D + 2);
-  constexpr bool PREFETCH = D * NT <= 128;
   __shared__ float lds_o[NW][16][LD];
   __shared__ float lds_m[NW][R], lds_l[NW][R];
   __shared__ int lds_flag;
@@ -983,42 +984,32 @@ __global__ __launch_bounds__(64 * ROWS_WAVES, 2) void kv4_attn_rows_kernel(Kv4At
       if (first_round) load_queries<D, NT>(a, t, q16, g, raw, q.pos);
       if (pages < 0 || pages >= a.w.num_pages) pages = -1;
       const int n = min((last - base + NW - 1) / NW, 64);
-      KStage<D> k0, k1;
-      VStage<D> v0, v1;
-      const auto load = [&](int i, KStage<D>& k, VStage<D>& v) {
-        const int page = __builtin_amdgcn_readlane(pages, i);
-        const Place pl = place_of<D>(a.w, head, max(page, 0), position_of(t, base + i * NW));
-        load_k<D>(pl, off, k);
-        load_v<D>(pl, off, v);
-      };
-      const auto compute = [&](int i, KStage<D>& k, VStage<D>& v) {
-        if (__builtin_amdgcn_readlane(pages, i) < 0) {
-          all_ok = false;
-          return;
-        }
-        const int t0 = position_of(t, base + i * NW);
-        f32x4_t sc[NT][2];
-        step_scores<D, FMT, NT>(k, q, c, sc);
-        if (step_at_edge(a, t, t0)) step_mask<D, NT>(a, t, t0, g, q, sc, v.s);
-        f16x8_t p[NT];
-        step_weights<D, FMT, NT>(sc, acc, p);
-        step_values<D, FMT, NT>(v, p, acc);
-      };
-      load(0, k0, v0);
+      KStage<D> ks;
+      VStage<D> vs;
+      int t0 = position_of(t, base), page = __builtin_amdgcn_readlane(pages, 0);
+      Place pl = place_of<D>(a.w, head, max(page, 0), t0);
+      load_k<D>(pl, off, ks);
+      load_v<D>(pl, off, vs);
       if (first_round) convert_queries<D, FMT, NT>(raw, q);
       first_round = false;
-      if constexpr (PREFETCH) {
-        for (int i = 0; i < n; i += 2) {
-          if (i + 1 < n) load(i + 1, k1, v1);
-          compute(i, k0, v0);
-          if (i + 1 >= n) break;
-          if (i + 2 < n) load(i + 2, k0, v0);
-          compute(i + 1, k1, v1);
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        if (page >= 0) {
+          f32x4_t sc[NT][2];
+          step_scores<D, FMT, NT>(ks, q, c, sc);
+          if (step_at_edge(a, t, t0)) step_mask<D, NT>(a, t, t0, g, q, sc, vs.s);
+          f16x8_t p[NT];
+          step_weights<D, FMT, NT>(sc, acc, p);
+          step_values<D, FMT, NT>(vs, p, acc);
+        } else {
+          all_ok = false;
         }
-      } else {
-        for (int i = 0; i < n; ++i) {
-          compute(i, k0, v0);
-          if (i + 1 < n) load(i + 1, k0, v0);
+        if (i + 1 < n) {
+          t0 = position_of(t, base + (i + 1) * NW);
+          page = __builtin_amdgcn_readlane(pages, i + 1);
+          pl = place_of<D>(a.w, head, max(page, 0), t0);
+          load_k<D>(pl, off, ks);
+          load_v<D>(pl, off, vs);
         }
       }
     }
@@ -1100,6 +1091,407 @@ __global__ __launch_bounds__(64 * ROWS_WAVES, 2) void kv4_attn_rows_kernel(Kv4At
   }
 }
 
+// ---- attention of many rows -------------------------------------------------------------------
+// A workgroup of 8 wavefronts holds 256 rows, 32 each, and walks the visible positions 64 at a
+// time.  The codes are decoded once for all rows, into LDS, while the matrix cores work on the
+// 64 positions before (two buffers, one barrier a turn):
+//   K: [D / 8][65] units of 16 bytes (8 d of one position; 65: banks), V: [8][D] units (8 positions
+//   of one d).  Both are the A operands of 32x32x16 matrix instructions as they lie.
+//   S^T = K Q^T, O^T += V^T P^T as above; row m of a 32-position A operand is position
+//   16 (m / 16) + 8 ((m / 4) % 2) + 4 ((m % 16) / 8) + m % 4, so that lane (q, h) ends up with
+//   positions 16 k + 8 h .. + 7 of row q in registers 8 k .. 8 k + 7: the B operand of O^T.
+constexpr int TILE_ROWS = 16 * KV4_TILE_NT, TILE_POS = 64, TILE_THREADS = 512, K_STRIDE = TILE_POS + 1;
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+// largest scale whose values and decode constants (INT4: 24 s) are finite in fp16, as bf16 bits
+__host__ __device__ constexpr uint32_t scale_limit(int fmt) { return fmt == FMT_INT4 ? 0x452Au : 0x462Au; }
+
+template <int D>
+struct TileStage {  // one thread's codes and scales of 64 positions
+  static constexpr int N = D / 64;  // dwords of K, and of V
+  uint32_t k[N], v[N];
+  uint16_t ks;
+  uint4 vs[(D + 127) / 128];
+};
+// Thread -> codes: K: position tid / 8, N consecutive dwords (one scale); V: the wavefront's block
+// of 8 positions, its i-th d at vd + v_step(i): two of every 128 columns, in one scale group.
+__host__ __device__ constexpr int v_step(int i) { return 16 * (i & 1) + 128 * (i >> 1); }
+template <int D>
+struct TileMap {
+  int tok, kd, blk, vd;
+  __device__ __forceinline__ TileMap(int tid) {
+    const int lane = tid & 63;
+    tok = tid >> 3;
+    kd = (tid & 7) * (D / 64);
+    blk = tid >> 6;
+    vd = D == 64 ? lane : (lane >> 4) * 32 + (lane & 15);
+  }
+};
+template <int D>
+__device__ __forceinline__ void tile_load(const Kv4Where& w, const Place& p, const Layout<D>& L,
+                                          const TileMap<D>& m, TileStage<D>& x) {
+  const int tok = m.tok & (KV4_STEP - 1), blk = m.blk & 3;
+  const uint32_t* k = reinterpret_cast<const uint32_t*>(p.codes + tok * (D / 2)) + m.kd;
+  if constexpr (D == 64) {
+    x.k[0] = k[0];
+  } else if constexpr (D == 128) {
+    const uint2 u = *reinterpret_cast<const uint2*>(k);
+    x.k[0] = u.x; x.k[1] = u.y;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(k);
+    x.k[0] = u.x; x.k[1] = u.y; x.k[2] = u.z; x.k[3] = u.w;
+  }
+  x.ks = *reinterpret_cast<const uint16_t*>(p.scales + L.ks +
+                                            2 * ((tok << L.n_shift) + ((8 * m.kd) >> w.group_shift)));
+  const uint32_t* v = reinterpret_cast<const uint32_t*>(p.codes + L.vc) + blk * D + m.vd;
+#pragma unroll
+  for (int i = 0; i < TileStage<D>::N; ++i) x.v[i] = v[v_step(i)];
+#pragma unroll
+  for (int e = 0; e < (D + 127) / 128; ++e)
+    x.vs[e] = *reinterpret_cast<const uint4*>(
+        p.scales + L.vs + 16 * ((blk << L.n_shift) + ((m.vd + 128 * e) >> w.group_shift)));
+}
+
+template <int D, int FMT>
+__global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4AttnArgs a) {
+  constexpr int R = TILE_ROWS, N = D / 64, NJ = D / 32, SIZE = R * (D + 2);
+  __shared__ uint4 lds_k[2][D / 8][K_STRIDE];
+  __shared__ uint4 lds_v[2][TILE_POS / 8][D];
+  __shared__ uint32_t lds_bad[2][8];  // positions of each block whose V scale is not usable
+  __shared__ int lds_flag;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int q32 = lane & 31, h = lane >> 5;
+  const int head = blockIdx.x % a.w.Hkv, part = blockIdx.x / a.w.Hkv;
+  const int part0 = head * a.n_parts;
+  const bool cut = a.part != nullptr;
+  int x = 0, end = 0, per = 1;
+  Spot spot;
+  Chunk chunk;
+  if (cut) {
+    const int total = line_length(a, R, chunk);
+    per = max((total + a.n_parts - 1) / a.n_parts, a.min_steps);
+    per = (per + 1) & ~1;
+    x = part * per;
+    end = min(x + per, total);
+    if (x >= end) return;
+  }
+  const Layout<D> L(a.w);
+  const TileMap<D> map(tid);
+  // row m of an A operand of K -> its position within 32
+  const int k_tok = 16 * (q32 >> 4) + 8 * ((q32 >> 2) & 1) + 4 * ((q32 >> 3) & 1) + (q32 & 3);
+  // the sign of the scale goes to Q; 1e-30 stands for a scale of 0 (equal weights all the same)
+  const float c = fmaxf(fabsf(a.scale * LOG2E), 1e-30f), move_by = MOVE / c;
+  Tile t;
+  while (true) {
+    int s0 = 0, s1;
+    bool whole = true;
+    if (cut) {
+      spot = find_spot(a, R, x, chunk);
+      tile_of(a, spot.s, spot.b, spot.tile, head, R, t);
+      s0 = x - spot.start;
+      s1 = min(end - spot.start, spot.steps);
+      whole = s0 == 0 && s1 == spot.steps;
+    } else {
+      // the longest tiles first
+      if (!tile_at(a, a.n_slots - 1 - part, head, R, t)) return;
+      s1 = t.n_steps;
+    }
+    if (t.s.len > t.s.cap && s0 == 0 && tid == 0) report(a.w.status, ST_LENGTH);
+    const int last = min(s1, t.n_steps), n_turns = last > s0 ? (last - s0 + 1) >> 1 : 0;
+    const int my0 = 32 * wave;  // first of the wavefront's rows
+    const bool busy = my0 < t.n_rho;
+    // positions of the wavefront's first and last row
+    const int p_first = t.s.len - t.s.n;
+    const int w_lo = p_first + row_of(a, t.rho0 + min(my0, t.n_rho - 1));
+    const int w_hi = p_first + row_of(a, t.rho0 + min(my0 + 31, t.n_rho - 1));
+    // pages and places of this part's steps; a step that is not there is far behind every row
+    int pages = -1, page_base = s0;
+    const auto load_pages = [&](int from) {
+      page_base = from;
+      const int step = min(from + lane, last - 1);
+      pages = a.w.table[(int64_t)t.b * a.w.max_pages + (position_of(t, step) >> a.w.page_shift)];
+      if (pages < 0 || pages >= a.w.num_pages) {
+        if (from + lane < last) report(a.w.status, ST_PAGE);
+        pages = -1;
+      }
+      if (from + lane >= last) pages = -1;
+    };
+    TileStage<D> st;
+    const auto load = [&](int step) {  // step: of the thread's half of the 64 positions
+      const int page = __builtin_amdgcn_readlane(pages, step - page_base);
+      const Place pl = place_of<D>(a.w, head, max(page, 0),
+                                   position_of(t, min(step, last - 1)));
+      tile_load<D>(a.w, pl, L, map, st);
+    };
+    const auto place_at = [&](int step) {
+      return __builtin_amdgcn_readlane(pages, step - page_base) < 0 ? 0x40000000
+                                                                    : position_of(t, step);
+    };
+    const auto edge_at = [&](int t0, int lo, int hi) {
+      return t0 + KV4_STEP - 1 > lo ||
+             (a.window > 0 && t0 <= hi - a.window && t0 + KV4_STEP > a.sinks);
+    };
+    const auto decode = [&](int buf, int t0) {  // t0: of the thread's half
+      const _Float16 s1 = (_Float16)bf16_to_f32(st.ks);
+      const f16x2_t s = {s1, s1}, s24 = s * (f16x2_t){(_Float16)-24.0f, (_Float16)-24.0f};
+      const f16x2_t s4[4] = {s, s, s, s}, z4[4] = {s24, s24, s24, s24};
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        lds_k[buf][map.kd + i][map.tok] =
+            __builtin_bit_cast(uint4, decode_f16<FMT>(st.k[i], s4, z4));
+      constexpr int NE = (D + 127) / 128;
+      uint32_t w[NE][4];
+#pragma unroll
+      for (int e = 0; e < NE; ++e) {
+        w[e][0] = st.vs[e].x; w[e][1] = st.vs[e].y; w[e][2] = st.vs[e].z; w[e][3] = st.vs[e].w;
+      }
+      if (edge_at(t0, t.p_lo, t.p_hi)) {
+        // scales that fp16 cannot take: cleared, and the rows that see them are told.  (In a step
+        // that all rows see whole they do their damage by themselves.)
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int e = 0; e < NE; ++e) {
+            const uint32_t b16 = ((i & 1) ? w[e][i / 2] >> 16 : w[e][i / 2]) & 0x7FFFu;
+            if (b16 > scale_limit(FMT)) {
+              bad |= 1u << i;
+              w[e][i / 2] &= (i & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+            }
+          }
+        uint32_t any = 0;
+        if (__ballot(bad != 0)) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) any |= __ballot((bad >> i) & 1) ? 1u << i : 0u;
+        }
+        if (lane == 0) lds_bad[buf][wave] = any;
+      }
+#pragma unroll
+      for (int e = 0; e < NE; ++e) {
+        f16x2_t vs[4], vs24[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int i0 = value_at<FMT>(2 * i), i1 = value_at<FMT>(2 * i + 1);
+          vs[i] = f16x2_t{
+              (_Float16)((i0 & 1) ? bf16_hi(w[e][i0 / 2]) : bf16_lo(w[e][i0 / 2])),
+              (_Float16)((i1 & 1) ? bf16_hi(w[e][i1 / 2]) : bf16_lo(w[e][i1 / 2]))};
+          vs24[i] = vs[i] * (f16x2_t){(_Float16)-24.0f, (_Float16)-24.0f};
+        }
+#pragma unroll
+        for (int i = 2 * e; i < N && i < 2 * e + 2; ++i)
+          lds_v[buf][map.blk][map.vd + v_step(i)] =
+              __builtin_bit_cast(uint4, decode_f16<FMT>(st.v[i], vs, vs24));
+      }
+    };
+
+    if (n_turns > 0) {
+      load_pages(s0);
+      load(s0 + (wave >> 2));
+    }
+    f16x8_t q[D / 16];
+    int pos;
+    {
+      const int rho = t.rho0 + my0 + q32;
+      const bool on = my0 + q32 < t.n_rho;
+      const int i = row_of(a, rho), hh = t.head * a.r + rho - i * a.r;
+      pos = on ? p_first + i : -1;
+      const uint16_t* p = a.q + (int64_t)(t.s.row0 + i) * a.q_stride + (int64_t)hh * D + 8 * h;
+      const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (on) u = *reinterpret_cast<const uint4*>(p + 16 * j);
+        const uint32_t uw[4] = {u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int d = value_at<FMT>(e);
+          q[j][e] = (_Float16)((d & 1) ? bf16_hi(uw[d / 2]) : bf16_lo(uw[d / 2]));
+        }
+      }
+    }
+    f32x16_t o[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[j][i] = 0.0f;
+    float m = -FLT_MAX, l = 0.0f;  // m: of the scores before scaling
+    if (n_turns > 0) decode(0, place_at(s0 + (wave >> 2)));
+    if (n_turns > 1) load(s0 + 2 + (wave >> 2));
+    __syncthreads();
+    for (int turn = 0; turn < n_turns; ++turn) {
+      const int buf = turn & 1, step = s0 + 2 * turn;
+      const int ta = place_at(step), tb = step + 1 < last ? place_at(step + 1) : 0x40000000;
+      // the next turn's place, before its pages may be replaced
+      const int t_next = turn + 1 < n_turns && step + 2 + (wave >> 2) < last
+                             ? place_at(step + 2 + (wave >> 2)) : 0x40000000;
+      const bool seen_a = ta <= w_hi, seen_b = tb <= w_hi;
+      const bool work = busy && (seen_a || seen_b);
+      f32x16_t sc[2];
+      if (work) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sc[u][i] = 0.0f;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j)
+            sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                __builtin_bit_cast(f16x8_t, lds_k[buf][2 * j + h][32 * u + k_tok]), q[j], sc[u], 0, 0,
+                0);
+        }
+      }
+      if (turn + 1 < n_turns) {
+        decode(buf ^ 1, t_next);
+        if (turn + 2 < n_turns) {
+          const int s2 = step + 4 + (wave >> 2);
+          if (step + 6 > page_base + 64) load_pages(step + 2);
+          load(s2);
+        }
+      }
+      if (work) {
+        const bool edge_wg = edge_at(ta, t.p_lo, t.p_hi) || edge_at(tb, t.p_lo, t.p_hi);
+        if (edge_wg) {
+          uint32_t bad[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int t0 = u ? tb : ta;
+            bad[u] = 0;
+            if (edge_at(t0, t.p_lo, t.p_hi))
+#pragma unroll
+              for (int b = 0; b < 4; ++b) bad[u] |= lds_bad[buf][4 * u + b] << (8 * b);
+            if (!edge_at(t0, w_lo, w_hi) && bad[u] == 0) continue;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int at = 16 * (i >> 3) + 8 * h + (i & 7), p = t0 + at;
+              const bool seen = p <= pos && (a.window == 0 || p > pos - a.window || p < a.sinks);
+              const float v = sc[u][i];
+              sc[u][i] = !seen ? -INFINITY : (bad[u] >> at) & 1 ? NAN : v;
+            }
+          }
+        }
+        float mx = fmaxf(sc[0][0], sc[1][0]);
+#pragma unroll
+        for (int i = 1; i < 16; ++i) mx = fmaxf(fmaxf(mx, sc[0][i]), sc[1][i]);
+        if (__ballot(mx > m + move_by)) {
+          mx = fmaxf(mx, __shfl_xor(mx, 32));
+          mx = fmaxf(mx, m);
+          const float f = __builtin_amdgcn_exp2f((m - mx) * c);
+          m = mx;
+          l *= f;
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) o[j] *= f;
+        }
+        const float ref = P_SHIFT - fmaxf(m * c, -FLT_MAX);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          f16x8_t p[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              e[i] = __builtin_amdgcn_exp2f(fmaf(sc[u][8 * k + i], c, ref));
+            l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) p[k][i] = (_Float16)e[value_at<FMT>(i)];
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+              o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+                  __builtin_bit_cast(f16x8_t, lds_v[buf][4 * u + 2 * k + h][32 * j + q32]), p[k], o[j],
+                  0, 0, 0);
+        }
+      }
+      __syncthreads();
+    }
+
+    l += __shfl_xor(l, 32);
+    const float m2 = l != 0.0f ? m * c : -FLT_MAX;  // in powers of 2, as the other kernel's
+    const int row = my0 + q32, place = 2 * (part0 + part) + (s0 == 0);
+    if (row < t.n_rho) {
+      if (whole) {
+        const float inv = row_inv(l);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            store_out4(a, t, D, row, 32 * j + 2 * i + 4 * h,
+                       make_float4(o[j][i], o[j][i + 1], o[j][i + 2], o[j][i + 3]), inv);
+        if (h == 0) store_lse(a, t, row, m2, l);
+      } else {
+        const __amdgpu_buffer_rsrc_t pr = part_rsrc(a.part);
+#pragma unroll
+        for (int j = 0; j < NJ; ++j)
+#pragma unroll
+          for (int i = 0; i < 16; i += 4)
+            st4_agent(pr, place * SIZE + row * D + 32 * j + 2 * i + 4 * h,
+                      make_float4(o[j][i], o[j][i + 1], o[j][i + 2], o[j][i + 3]));
+        if (h == 0) {
+          st_sc1(a.part, (size_t)place * SIZE + R * D + row, m2);
+          st_sc1(a.part, (size_t)place * SIZE + R * D + R + row, l);
+        }
+      }
+    }
+    if (!cut) return;
+    if (!whole) {
+      const int first = spot.start / per, n = (spot.start + spot.steps - 1) / per - first + 1;
+      if (last_arriver(a.counters + part0 + first, (unsigned)n, &lds_flag)) {
+        // every thread keeps D / 8 columns of 4 rows apart: 16 bytes at a time, part by part
+        const __amdgpu_buffer_rsrc_t pr = part_rsrc(a.part);
+        constexpr int LR = D / 4, RS = TILE_THREADS / LR;  // lanes of a row, rows at once
+        for (int r0 = tid / LR; r0 < t.n_rho; r0 += 4 * RS) {
+          const int d = 4 * (tid % LR);
+          float mm[4], ll[4];
+          float4 oo[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            mm[u] = -FLT_MAX;
+            ll[u] = 0.0f;
+            oo[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          }
+          for (int k = 0; k < n; ++k) {
+            const int at = (2 * (part0 + first + k) + (k == 0)) * SIZE;
+            float4 v[4];
+            float pm[4], pl[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int rr = min(r0 + u * RS, t.n_rho - 1);
+              v[u] = ld4_agent(pr, at + rr * D + d);
+              pm[u] = __uint_as_float(
+                  __builtin_amdgcn_raw_buffer_load_b32(pr, (at + R * D + rr) * 4, 0, 16));
+              pl[u] = __uint_as_float(
+                  __builtin_amdgcn_raw_buffer_load_b32(pr, (at + R * D + R + rr) * 4, 0, 16));
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const float mx = fmaxf(mm[u], pm[u]);
+              const float f0 = __builtin_amdgcn_exp2f(mm[u] - mx), f = __builtin_amdgcn_exp2f(pm[u] - mx);
+              mm[u] = mx;
+              ll[u] = ll[u] * f0 + pl[u] * f;
+              oo[u].x = oo[u].x * f0 + v[u].x * f; oo[u].y = oo[u].y * f0 + v[u].y * f;
+              oo[u].z = oo[u].z * f0 + v[u].z * f; oo[u].w = oo[u].w * f0 + v[u].w * f;
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int rr = r0 + u * RS;
+            if (rr < t.n_rho) {
+              store_out4(a, t, D, rr, d, oo[u], row_inv(ll[u]));
+              if (d == 0) store_lse(a, t, rr, mm[u], ll[u]);
+            }
+          }
+        }
+        if (tid == 0) st_cnt(a.counters + part0 + first, 0u);
+      }
+    }
+    x = spot.start + s1;
+    if (x >= end) return;
+    __syncthreads();
+  }
+}
+
 template <int D, int FMT>
 hipError_t launch_rows(const Kv4RowsArgs& a, hipStream_t st) {
   const int64_t units = 2 * (int64_t)a.w.Hkv * ((a.w.T >> 3) + 2 * (int64_t)a.w.B);
@@ -1114,6 +1506,10 @@ hipError_t launch_rows(const Kv4RowsArgs& a, hipStream_t st) {
 template <int D, int FMT>
 hipError_t launch_attn(const Kv4AttnArgs& a, hipStream_t st) {
   const unsigned grid = (unsigned)a.w.Hkv * (a.part ? a.n_parts : a.n_slots);
+  if (a.nt == KV4_TILE_NT) {
+    kv4_attn_tiles_kernel<D, FMT><<<grid, TILE_THREADS, 0, st>>>(a);
+    return hipGetLastError();
+  }
   if constexpr (D <= 128) {
     if (a.nt == 2) {
       kv4_attn_rows_kernel<D, FMT, 2><<<grid, 64 * ROWS_WAVES, 0, st>>>(a);
