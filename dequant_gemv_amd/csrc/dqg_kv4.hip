@@ -537,11 +537,16 @@ __device__ __forceinline__ f16x8_t decode_f16(uint32_t w, const f16x2_t (&s)[4],
                                               const f16x2_t (&s24)[4]) {
   f16x2_t p[4];
   if constexpr (FMT == FMT_INT4) {
+    // (the mask in a vector and the exponent in a scalar register: and_or takes them as one
+    // instruction, where two literals make it two)
+    uint32_t mask = 0x03C003C0u, sixteen = 0x4C004C00u;
+    asm("" : "+v"(mask));
+    asm("" : "+s"(sixteen));
     const uint32_t u[4] = {w << 6, w << 2, w >> 2, w >> 6};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      p[i] = __builtin_elementwise_fma(
-          __builtin_bit_cast(f16x2_t, (u[i] & 0x03C003C0u) | 0x4C004C00u), s[i], s24[i]);
+      p[i] = __builtin_elementwise_fma(__builtin_bit_cast(f16x2_t, (u[i] & mask) | sixteen), s[i],
+                                       s24[i]);
   } else {
     p[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0) * s[0];
     p[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1) * s[1];
@@ -1106,6 +1111,15 @@ typedef float f32x16_t __attribute__((ext_vector_type(16)));
 // largest scale whose values and decode constants (INT4: 24 s) are finite in fp16, as bf16 bits
 __host__ __device__ constexpr uint32_t scale_limit(int fmt) { return fmt == FMT_INT4 ? 0x452Au : 0x462Au; }
 
+// halves of a dword of V scales that are above the limit, as nonzero halves
+template <int FMT>
+__device__ __forceinline__ uint32_t above_limit(uint32_t w) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  const u16x2 lim = {(unsigned short)scale_limit(FMT), (unsigned short)scale_limit(FMT)};
+  return __builtin_bit_cast(
+      uint32_t, __builtin_elementwise_sub_sat(__builtin_bit_cast(u16x2, w & 0x7FFF7FFFu), lim));
+}
+
 template <int D>
 struct TileStage {  // one thread's codes and scales of 64 positions
   static constexpr int N = D / 64;  // dwords of K, and of V
@@ -1150,6 +1164,75 @@ __device__ __forceinline__ void tile_load(const Kv4Where& w, const Place& p, con
   for (int e = 0; e < (D + 127) / 128; ++e)
     x.vs[e] = *reinterpret_cast<const uint4*>(
         p.scales + L.vs + 16 * ((blk << L.n_shift) + ((m.vd + 128 * e) >> w.group_shift)));
+}
+
+// Keeps the order of what is written on both sides: left alone, the compiler reads one operand from
+// LDS, waits for it, multiplies and reads the next into the same registers.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// S^T of 64 positions; k: the lane's unit of the first operand.  Four operands are read while the
+// four before them are multiplied.
+template <int D>
+__device__ __forceinline__ void tile_scores(const uint4* k, const f16x8_t (&q)[D / 16],
+                                            f32x16_t (&sc)[2]) {
+  constexpr int G = D / 32;  // groups of 4 operands: 2 times 16 d, 2 times 32 positions
+  const auto read = [&](int n, uint4 (&x)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = k[2 * (2 * n + (i >> 1)) * K_STRIDE + 32 * (i & 1)];
+  };
+  uint4 x[2][4];
+  read(0, x[0]);
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sc[u][i] = 0.0f;
+#pragma unroll
+  for (int n = 0; n < G; ++n) {
+    keep_order();
+    if (n + 1 < G) read(n + 1, x[(n + 1) & 1]);
+    keep_order();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      sc[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+          __builtin_bit_cast(f16x8_t, x[n & 1][i]), q[2 * n + (i >> 1)], sc[i & 1], 0, 0, 0);
+  }
+  keep_order();
+}
+// Weights of 64 positions and O^T += V^T P^T; v: the lane's unit of the first operand.
+template <int D, int FMT>
+__device__ __forceinline__ void tile_values(const uint4* v, const f32x16_t (&sc)[2], float c, float ref,
+                                            float& l, f32x16_t (&o)[D / 32]) {
+  constexpr int NJ = D / 32;
+  const auto read = [&](int b, uint4 (&x)[NJ]) {
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) x[j] = v[2 * b * D + 32 * j];
+  };
+  const auto weights = [&](int b) {  // of 16 positions
+    float e[8];
+    f16x8_t p;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      e[i] = __builtin_amdgcn_exp2f(fmaf(sc[b >> 1][8 * (b & 1) + i], c, ref));
+    l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) p[i] = (_Float16)e[value_at<FMT>(i)];
+    return p;
+  };
+  uint4 x[2][NJ];
+  read(0, x[0]);
+  keep_order();
+  f16x8_t p = weights(0);
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    keep_order();
+    if (b < 3) read(b + 1, x[(b + 1) & 1]);
+    keep_order();
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, x[b & 1][j]), p,
+                                                    o[j], 0, 0, 0);
+    if (b < 3) p = weights(b + 1);
+  }
 }
 
 template <int D, int FMT>
@@ -1249,21 +1332,23 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
       if (edge_at(t0, t.p_lo, t.p_hi)) {
         // scales that fp16 cannot take: cleared, and the rows that see them are told.  (In a step
         // that all rows see whole they do their damage by themselves.)
-        uint32_t bad = 0;
+        uint32_t over[4], any_over = 0, any = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i) {
+          over[i] = above_limit<FMT>(w[0][i]);
 #pragma unroll
-          for (int e = 0; e < NE; ++e) {
-            const uint32_t b16 = ((i & 1) ? w[e][i / 2] >> 16 : w[e][i / 2]) & 0x7FFFu;
-            if (b16 > scale_limit(FMT)) {
-              bad |= 1u << i;
-              w[e][i / 2] &= (i & 1) ? 0x0000FFFFu : 0xFFFF0000u;
-            }
+          for (int e = 1; e < NE; ++e) over[i] |= above_limit<FMT>(w[e][i]);
+          any_over |= over[i];
+        }
+        if (__ballot(any_over != 0)) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t half = (i & 1) ? 0xFFFF0000u : 0x0000FFFFu;
+            const bool bad = (over[i / 2] & half) != 0;
+            any |= __ballot(bad) ? 1u << i : 0u;
+#pragma unroll
+            for (int e = 0; e < NE; ++e) w[e][i / 2] &= bad ? ~half : ~0u;
           }
-        uint32_t any = 0;
-        if (__ballot(bad != 0)) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) any |= __ballot((bad >> i) & 1) ? 1u << i : 0u;
         }
         if (lane == 0) lds_bad[buf][wave] = any;
       }
@@ -1328,18 +1413,7 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
       const bool seen_a = ta <= w_hi, seen_b = tb <= w_hi;
       const bool work = busy && (seen_a || seen_b);
       f32x16_t sc[2];
-      if (work) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) sc[u][i] = 0.0f;
-#pragma unroll
-          for (int j = 0; j < D / 16; ++j)
-            sc[u] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                __builtin_bit_cast(f16x8_t, lds_k[buf][2 * j + h][32 * u + k_tok]), q[j], sc[u], 0, 0,
-                0);
-        }
-      }
+      if (work) tile_scores<D>(&lds_k[buf][h][k_tok], q, sc);
       if (turn + 1 < n_turns) {
         decode(buf ^ 1, t_next);
         if (turn + 2 < n_turns) {
@@ -1349,23 +1423,29 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
         }
       }
       if (work) {
-        const bool edge_wg = edge_at(ta, t.p_lo, t.p_hi) || edge_at(tb, t.p_lo, t.p_hi);
-        if (edge_wg) {
-          uint32_t bad[2];
+        if (edge_at(ta, t.p_lo, t.p_hi) || edge_at(tb, t.p_lo, t.p_hi)) {
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int t0 = u ? tb : ta;
-            bad[u] = 0;
+            uint32_t bad = 0;
             if (edge_at(t0, t.p_lo, t.p_hi))
 #pragma unroll
-              for (int b = 0; b < 4; ++b) bad[u] |= lds_bad[buf][4 * u + b] << (8 * b);
-            if (!edge_at(t0, w_lo, w_hi) && bad[u] == 0) continue;
+              for (int b = 0; b < 4; ++b) bad |= lds_bad[buf][4 * u + b] << (8 * b);
+            if (!edge_at(t0, w_lo, w_hi) && bad == 0) continue;
+            // against the constant offset of a register's position
+            const int to = pos - t0 - 8 * h, from = a.window > 0 ? to - a.window : -1000;
+            const int first = a.sinks - t0 - 8 * h;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const int at = 16 * (i >> 3) + 8 * h + (i & 7), p = t0 + at;
-              const bool seen = p <= pos && (a.window == 0 || p > pos - a.window || p < a.sinks);
-              const float v = sc[u][i];
-              sc[u][i] = !seen ? -INFINITY : (bad[u] >> at) & 1 ? NAN : v;
+              const int at = 16 * (i >> 3) + (i & 7);
+              const bool seen = at <= to && (at > from || at < first);
+              sc[u][i] = seen ? sc[u][i] : -INFINITY;
+            }
+            if (bad) {
+              const uint32_t mine = bad >> (8 * h);
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if ((mine >> (16 * (i >> 3) + (i & 7))) & 1 && sc[u][i] != -INFINITY) sc[u][i] = NAN;
             }
           }
         }
@@ -1381,28 +1461,7 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
 #pragma unroll
           for (int j = 0; j < NJ; ++j) o[j] *= f;
         }
-        const float ref = P_SHIFT - fmaxf(m * c, -FLT_MAX);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          f16x8_t p[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float e[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              e[i] = __builtin_amdgcn_exp2f(fmaf(sc[u][8 * k + i], c, ref));
-            l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[k][i] = (_Float16)e[value_at<FMT>(i)];
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-              o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                  __builtin_bit_cast(f16x8_t, lds_v[buf][4 * u + 2 * k + h][32 * j + q32]), p[k], o[j],
-                  0, 0, 0);
-        }
+        tile_values<D, FMT>(&lds_v[buf][h][q32], sc, c, P_SHIFT - fmaxf(m * c, -FLT_MAX), l, o);
       }
       __syncthreads();
     }
