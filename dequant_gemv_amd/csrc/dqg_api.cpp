@@ -709,7 +709,7 @@ size_t kv4_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int m
   if (!kv4_attn_sizes_ok(T, B, Hq, Hkv, D) || max_kv_len < 1 || max_kv_len > (1 << 30)) return 0;
   if (max_kv_len <= kKv4MinSteps * dqg::KV4_STEP) return 0;
   return up256(kv4_counter_bytes() + 2 * (size_t)Hkv * kv4_parts(Hkv) * sizeof(float) *
-                                         dqg::kv4_part_floats(dqg::KV4_TILE_NT, D));
+                                         dqg::kv4_part_floats(dqg::kv4_tile_nt(D), D));
 }
 
 int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32_t* cu_rows,
@@ -759,7 +759,7 @@ int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32
                                                                            min_steps));
     // many-row tiles are cut only where they are too few to fill the GPU by themselves (two rounds);
     // places on the line are 32-bit
-    const bool cut = workspace && (nt < dqg::KV4_TILE_NT || tiles < 2 * kKv4Resident) &&
+    const bool cut = workspace && (nt < dqg::kv4_tile_nt(D) || tiles < 2 * kKv4Resident) &&
                      (long long)a.n_slots * (cap / dqg::KV4_STEP) < (1LL << 30);
     a.counters = cut ? static_cast<unsigned*>(workspace) : nullptr;
     a.part = cut ? reinterpret_cast<float*>(static_cast<char*>(workspace) + kv4_counter_bytes())
@@ -774,7 +774,7 @@ int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32
     rc = launch(nt, 0, few, kKv4MinSteps);
     if (rc != DQG_OK) return rc;
   }
-  return launch(dqg::KV4_TILE_NT, B > 1 ? few : 0, INT_MAX, kKv4MinTileSteps);
+  return launch(dqg::kv4_tile_nt(D), B > 1 ? few : 0, INT_MAX, kKv4MinTileSteps);
 }
 
 int packed_dequant_f32(const uint8_t* w, const uint16_t* s, int K, int N, int group,

@@ -159,10 +159,11 @@ struct Kv4AttnArgs {
   int window, sinks;
   int n_slots, n_parts;  // row-tile slots; parts of a head's steps
   int min_steps;         // steps of a part, at least
-  int nt;                // 16-row tiles per workgroup: 1, 2 or KV4_TILE_NT
+  int nt;                // 16-row tiles per workgroup: 1, 2 or kv4_tile_nt(D)
   int rows_over, rows_to;  // the launch takes sequences of more rows than the one, up to the other
 };
-constexpr int KV4_TILE_NT = 16;  // of the kernel for many rows
+// 16-row tiles of a workgroup of the kernel for many rows
+constexpr int kv4_tile_nt(int D) { return D > 128 ? 8 : 16; }
 constexpr int KV4_STEP = 32;  // tokens of one step of a wavefront
 hipError_t launch_kv4_write(const Kv4RowsArgs& a, int D, int fmt, hipStream_t st);
 hipError_t launch_kv4_read(const Kv4RowsArgs& a, int D, int fmt, hipStream_t st);

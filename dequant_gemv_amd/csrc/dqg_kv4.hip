@@ -1097,15 +1097,29 @@ __global__ __launch_bounds__(64 * ROWS_WAVES, 2) void kv4_attn_rows_kernel(Kv4At
 }
 
 // ---- attention of many rows -------------------------------------------------------------------
-// A workgroup of 8 wavefronts holds 256 rows, 32 each, and walks the visible positions 64 at a
-// time.  The codes are decoded once for all rows, into LDS, while the matrix cores work on the
-// 64 positions before (two buffers, one barrier a turn):
+// A workgroup of 8 wavefronts walks the visible positions 64 at a time (a turn).  The codes are
+// decoded once for all its rows, into LDS:
 //   K: [D / 8][65] units of 16 bytes (8 d of one position; 65: banks), V: [8][D] units (8 positions
 //   of one d).  Both are the A operands of 32x32x16 matrix instructions as they lie.
 //   S^T = K Q^T, O^T += V^T P^T as above; row m of a 32-position A operand is position
 //   16 (m / 16) + 8 ((m / 4) % 2) + 4 ((m % 16) / 8) + m % 4, so that lane (q, h) ends up with
 //   positions 16 k + 8 h .. + 7 of row q in registers 8 k .. 8 k + 7: the B operand of O^T.
-constexpr int TILE_ROWS = 16 * KV4_TILE_NT, TILE_POS = 64, TILE_THREADS = 512, K_STRIDE = TILE_POS + 1;
+// D <= 128: a wavefront holds 32 rows whole.  D = 256: two wavefronts hold 32 rows; each takes
+// half of a turn's positions for S and half of the columns of O, whose sums would not fit
+// otherwise, and they trade row maxima and weights through LDS.
+//
+// A turn of a wavefront is two phases, a barrier behind each: M, the matrix instructions (S of
+// this turn, O of the turn before), and A, the arithmetic (weights of this turn, decoding).
+// Wavefronts 0-3 and 4-7, one of each on every SIMD, are in opposite phases, so that the matrix
+// cores and the vector ALUs work at the same time.
+// Slot 2 t (between two barriers) is phase M of turn t for group 0 and phase A of turn t - 1 for
+// group 1, slot 2 t + 1 the other way round; the phases A of both slots decode K of turn t + 1 and V
+// of turn t, each thread its share.  (K of turn t + 1 takes the place of turn t - 1's, last read
+// in slot 2 t - 1, and is first read in slot 2 t + 2; V of turn t that of turn t - 2's, last read in
+// slot 2 t - 1, first read in slot 2 t + 2.)
+constexpr int TILE_POS = 64, TILE_THREADS = 512, K_STRIDE = TILE_POS + 1;
+__host__ __device__ constexpr int tile_halves(int D) { return D > 128 ? 2 : 1; }
+__host__ __device__ constexpr int tile_rows(int D) { return 16 * kv4_tile_nt(D); }
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 // largest scale whose values and decode constants (INT4: 24 s) are finite in fp16, as bf16 bits
@@ -1121,11 +1135,11 @@ __device__ __forceinline__ uint32_t above_limit(uint32_t w) {
 }
 
 template <int D>
-struct TileStage {  // one thread's codes and scales of 64 positions
-  static constexpr int N = D / 64;  // dwords of K, and of V
+struct TileStage {  // one thread's codes and scales: K and V scales of a turn, V of the one before
+  static constexpr int N = D / 64, NE = (D + 127) / 128;  // dwords of K, and of V
   uint32_t k[N], v[N];
   uint16_t ks;
-  uint4 vs[(D + 127) / 128];
+  uint4 vs[NE];
 };
 // Thread -> codes: K: position tid / 8, N consecutive dwords (one scale); V: the wavefront's block
 // of 8 positions, its i-th d at vd + v_step(i): two of every 128 columns, in one scale group.
@@ -1142,8 +1156,8 @@ struct TileMap {
   }
 };
 template <int D>
-__device__ __forceinline__ void tile_load(const Kv4Where& w, const Place& p, const Layout<D>& L,
-                                          const TileMap<D>& m, TileStage<D>& x) {
+__device__ __forceinline__ void tile_load_k(const Kv4Where& w, const Place& p, const Layout<D>& L,
+                                            const TileMap<D>& m, TileStage<D>& x) {
   const int tok = m.tok & (KV4_STEP - 1), blk = m.blk & 3;
   const uint32_t* k = reinterpret_cast<const uint32_t*>(p.codes + tok * (D / 2)) + m.kd;
   if constexpr (D == 64) {
@@ -1157,33 +1171,37 @@ __device__ __forceinline__ void tile_load(const Kv4Where& w, const Place& p, con
   }
   x.ks = *reinterpret_cast<const uint16_t*>(p.scales + L.ks +
                                             2 * ((tok << L.n_shift) + ((8 * m.kd) >> w.group_shift)));
-  const uint32_t* v = reinterpret_cast<const uint32_t*>(p.codes + L.vc) + blk * D + m.vd;
 #pragma unroll
-  for (int i = 0; i < TileStage<D>::N; ++i) x.v[i] = v[v_step(i)];
-#pragma unroll
-  for (int e = 0; e < (D + 127) / 128; ++e)
+  for (int e = 0; e < TileStage<D>::NE; ++e)
     x.vs[e] = *reinterpret_cast<const uint4*>(
         p.scales + L.vs + 16 * ((blk << L.n_shift) + ((m.vd + 128 * e) >> w.group_shift)));
+}
+template <int D>
+__device__ __forceinline__ void tile_load_v(const Place& p, const Layout<D>& L, const TileMap<D>& m,
+                                            TileStage<D>& x) {
+  const uint32_t* v = reinterpret_cast<const uint32_t*>(p.codes + L.vc) + (m.blk & 3) * D + m.vd;
+#pragma unroll
+  for (int i = 0; i < TileStage<D>::N; ++i) x.v[i] = v[v_step(i)];
 }
 
 // Keeps the order of what is written on both sides: left alone, the compiler reads one operand from
 // LDS, waits for it, multiplies and reads the next into the same registers.
 __device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
 
-// S^T of 64 positions; k: the lane's unit of the first operand.  Four operands are read while the
-// four before them are multiplied.
-template <int D>
+// S^T of NU times 32 positions; k: the lane's unit of the first operand.  Four operands are read
+// while the four before them are multiplied.
+template <int D, int NU>
 __device__ __forceinline__ void tile_scores(const uint4* k, const f16x8_t (&q)[D / 16],
-                                            f32x16_t (&sc)[2]) {
-  constexpr int G = D / 32;  // groups of 4 operands: 2 times 16 d, 2 times 32 positions
+                                            f32x16_t (&sc)[NU]) {
+  constexpr int J = 4 / NU, G = D / 16 / J;  // groups of 4 operands: J times 16 d
   const auto read = [&](int n, uint4 (&x)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = k[2 * (2 * n + (i >> 1)) * K_STRIDE + 32 * (i & 1)];
+    for (int i = 0; i < 4; ++i) x[i] = k[2 * (J * n + i / NU) * K_STRIDE + 32 * (i % NU)];
   };
   uint4 x[2][4];
   read(0, x[0]);
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
+  for (int u = 0; u < NU; ++u)
 #pragma unroll
     for (int i = 0; i < 16; ++i) sc[u][i] = 0.0f;
 #pragma unroll
@@ -1193,57 +1211,106 @@ __device__ __forceinline__ void tile_scores(const uint4* k, const f16x8_t (&q)[D
     keep_order();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      sc[i & 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-          __builtin_bit_cast(f16x8_t, x[n & 1][i]), q[2 * n + (i >> 1)], sc[i & 1], 0, 0, 0);
+      sc[i % NU] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+          __builtin_bit_cast(f16x8_t, x[n & 1][i]), q[J * n + i / NU], sc[i % NU], 0, 0, 0);
   }
   keep_order();
 }
-// Weights of 64 positions and O^T += V^T P^T; v: the lane's unit of the first operand.
-template <int D, int FMT>
-__device__ __forceinline__ void tile_values(const uint4* v, const f32x16_t (&sc)[2], float c, float ref,
-                                            float& l, f32x16_t (&o)[D / 32]) {
-  constexpr int NJ = D / 32;
+// O^T += V^T P^T of 64 positions; v: the lane's unit of the first operand, weights(b): of the b-th
+// 16 positions.
+template <int D, int NJ, class P>
+__device__ __forceinline__ void tile_values(const uint4* v, P weights, f32x16_t (&o)[NJ]) {
   const auto read = [&](int b, uint4 (&x)[NJ]) {
 #pragma unroll
     for (int j = 0; j < NJ; ++j) x[j] = v[2 * b * D + 32 * j];
   };
-  const auto weights = [&](int b) {  // of 16 positions
-    float e[8];
-    f16x8_t p;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      e[i] = __builtin_amdgcn_exp2f(fmaf(sc[b >> 1][8 * (b & 1) + i], c, ref));
-    l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = (_Float16)e[value_at<FMT>(i)];
-    return p;
-  };
   uint4 x[2][NJ];
   read(0, x[0]);
-  keep_order();
   f16x8_t p = weights(0);
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     keep_order();
-    if (b < 3) read(b + 1, x[(b + 1) & 1]);
+    f16x8_t next = p;
+    if (b < 3) {
+      read(b + 1, x[(b + 1) & 1]);
+      next = weights(b + 1);
+    }
     keep_order();
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
       o[j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, x[b & 1][j]), p,
                                                     o[j], 0, 0, 0);
-    if (b < 3) p = weights(b + 1);
+    p = next;
+  }
+  keep_order();
+}
+
+// Joins the partials of a tile of many rows: few parts, so a thread keeps 4 columns of 4 rows and
+// goes through the parts in order.
+template <int D, int R>
+__device__ __forceinline__ void join_tiles(const Kv4AttnArgs& a, const Tile& t, int part0, int first,
+                                           int n, int tid) {
+  constexpr int LR = D / 4, RS = TILE_THREADS / LR, SIZE = R * (D + 2);
+  const __amdgpu_buffer_rsrc_t pr = part_rsrc(a.part);
+  const int d = 4 * (tid % LR);
+  for (int r0 = tid / LR; r0 < t.n_rho; r0 += 4 * RS) {
+    float mm[4], ll[4];
+    float4 oo[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      mm[u] = -FLT_MAX;
+      ll[u] = 0.0f;
+      oo[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    for (int k = 0; k < n; ++k) {
+      const int at = (2 * (part0 + first + k) + (k == 0)) * SIZE;
+      float4 v[4];
+      float pm[4], pl[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int rr = min(r0 + u * RS, t.n_rho - 1);
+        v[u] = ld4_agent(pr, at + rr * D + d);
+        pm[u] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(pr, (at + R * D + rr) * 4, 0, 16));
+        pl[u] = __uint_as_float(
+            __builtin_amdgcn_raw_buffer_load_b32(pr, (at + R * D + R + rr) * 4, 0, 16));
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float mx = fmaxf(mm[u], pm[u]);
+        const float f0 = __builtin_amdgcn_exp2f(mm[u] - mx), f = __builtin_amdgcn_exp2f(pm[u] - mx);
+        mm[u] = mx;
+        ll[u] = ll[u] * f0 + pl[u] * f;
+        oo[u].x = oo[u].x * f0 + v[u].x * f; oo[u].y = oo[u].y * f0 + v[u].y * f;
+        oo[u].z = oo[u].z * f0 + v[u].z * f; oo[u].w = oo[u].w * f0 + v[u].w * f;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int rr = r0 + u * RS;
+      if (rr < t.n_rho) {
+        store_out4(a, t, D, rr, d, oo[u], row_inv(ll[u]));
+        if (d == 0) store_lse(a, t, rr, mm[u], ll[u]);
+      }
+    }
   }
 }
 
 template <int D, int FMT>
 __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4AttnArgs a) {
-  constexpr int R = TILE_ROWS, N = D / 64, NJ = D / 32, SIZE = R * (D + 2);
+  constexpr int HV = tile_halves(D), R = tile_rows(D), NU = 2 / HV, N = D / 64, NJ = D / 32 / HV;
+  constexpr int NE = TileStage<D>::NE, SIZE = R * (D + 2);
+  constexpr int NOWHERE = 0x40000000;  // place of a step that is not there: behind every row
   __shared__ uint4 lds_k[2][D / 8][K_STRIDE];
   __shared__ uint4 lds_v[2][TILE_POS / 8][D];
-  __shared__ uint32_t lds_bad[2][8];  // positions of each block whose V scale is not usable
+  __shared__ uint32_t lds_bad[4][8];  // positions of each block whose V scale is not usable
+  __shared__ uint4 lds_p[HV == 2 ? 4 : 1][HV == 2 ? 4 : 1][64];
+  __shared__ float lds_m[HV == 2 ? 4 : 1][2][32];
   __shared__ int lds_flag;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int group = wave >> 2;
+  // the wavefront's 32 rows, and (D = 256) its half of the positions and columns
+  const int rows32 = HV == 2 ? 2 * group + ((wave & 3) >> 1) : wave, half = HV == 2 ? wave & 1 : 0;
   const int q32 = lane & 31, h = lane >> 5;
   const int head = blockIdx.x % a.w.Hkv, part = blockIdx.x / a.w.Hkv;
   const int part0 = head * a.n_parts;
@@ -1282,13 +1349,13 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
     }
     if (t.s.len > t.s.cap && s0 == 0 && tid == 0) report(a.w.status, ST_LENGTH);
     const int last = min(s1, t.n_steps), n_turns = last > s0 ? (last - s0 + 1) >> 1 : 0;
-    const int my0 = 32 * wave;  // first of the wavefront's rows
+    const int my0 = 32 * rows32;  // first of the wavefront's rows
     const bool busy = my0 < t.n_rho;
     // positions of the wavefront's first and last row
     const int p_first = t.s.len - t.s.n;
     const int w_lo = p_first + row_of(a, t.rho0 + min(my0, t.n_rho - 1));
     const int w_hi = p_first + row_of(a, t.rho0 + min(my0 + 31, t.n_rho - 1));
-    // pages and places of this part's steps; a step that is not there is far behind every row
+    // pages of 64 steps from page_base on, one a lane; -1: no such step, or no such page
     int pages = -1, page_base = s0;
     const auto load_pages = [&](int from) {
       page_base = from;
@@ -1300,58 +1367,62 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
       }
       if (from + lane >= last) pages = -1;
     };
-    TileStage<D> st;
-    const auto load = [&](int step) {  // step: of the thread's half of the 64 positions
-      const int page = __builtin_amdgcn_readlane(pages, step - page_base);
-      const Place pl = place_of<D>(a.w, head, max(page, 0),
-                                   position_of(t, min(step, last - 1)));
-      tile_load<D>(a.w, pl, L, map, st);
+    // the place of the u-th half of a turn
+    const auto place_at = [&](int turn, int u) {
+      const int step = s0 + 2 * turn + u;
+      if (step >= last || __builtin_amdgcn_readlane(pages, step - page_base) < 0) return NOWHERE;
+      return position_of(t, step);
     };
-    const auto place_at = [&](int step) {
-      return __builtin_amdgcn_readlane(pages, step - page_base) < 0 ? 0x40000000
-                                                                    : position_of(t, step);
+    // where a thread reads its codes of a turn (what is not there is read from some page: hidden)
+    const auto codes_at = [&](int turn) {
+      const int step = min(s0 + 2 * turn + group, last - 1);
+      const int page = __builtin_amdgcn_readlane(pages, step - page_base);
+      return place_of<D>(a.w, head, max(page, 0), position_of(t, step));
     };
     const auto edge_at = [&](int t0, int lo, int hi) {
       return t0 + KV4_STEP - 1 > lo ||
              (a.window > 0 && t0 <= hi - a.window && t0 + KV4_STEP > a.sinks);
     };
-    const auto decode = [&](int buf, int t0) {  // t0: of the thread's half
+    TileStage<D> st;
+    uint32_t vs_now[NE][4];  // V scales of the turn whose V is decoded next
+    const auto decode_k = [&](int turn) {  // K of a turn, and its V scales to vs_now
       const _Float16 s1 = (_Float16)bf16_to_f32(st.ks);
       const f16x2_t s = {s1, s1}, s24 = s * (f16x2_t){(_Float16)-24.0f, (_Float16)-24.0f};
       const f16x2_t s4[4] = {s, s, s, s}, z4[4] = {s24, s24, s24, s24};
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        lds_k[buf][map.kd + i][map.tok] =
+        lds_k[turn & 1][map.kd + i][map.tok] =
             __builtin_bit_cast(uint4, decode_f16<FMT>(st.k[i], s4, z4));
-      constexpr int NE = (D + 127) / 128;
-      uint32_t w[NE][4];
 #pragma unroll
       for (int e = 0; e < NE; ++e) {
-        w[e][0] = st.vs[e].x; w[e][1] = st.vs[e].y; w[e][2] = st.vs[e].z; w[e][3] = st.vs[e].w;
+        vs_now[e][0] = st.vs[e].x; vs_now[e][1] = st.vs[e].y;
+        vs_now[e][2] = st.vs[e].z; vs_now[e][3] = st.vs[e].w;
       }
-      if (edge_at(t0, t.p_lo, t.p_hi)) {
+      if (edge_at(place_at(turn, group), t.p_lo, t.p_hi)) {
         // scales that fp16 cannot take: cleared, and the rows that see them are told.  (In a step
         // that all rows see whole they do their damage by themselves.)
         uint32_t over[4], any_over = 0, any = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          over[i] = above_limit<FMT>(w[0][i]);
+          over[i] = above_limit<FMT>(vs_now[0][i]);
 #pragma unroll
-          for (int e = 1; e < NE; ++e) over[i] |= above_limit<FMT>(w[e][i]);
+          for (int e = 1; e < NE; ++e) over[i] |= above_limit<FMT>(vs_now[e][i]);
           any_over |= over[i];
         }
         if (__ballot(any_over != 0)) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint32_t half = (i & 1) ? 0xFFFF0000u : 0x0000FFFFu;
-            const bool bad = (over[i / 2] & half) != 0;
+            const uint32_t h16 = (i & 1) ? 0xFFFF0000u : 0x0000FFFFu;
+            const bool bad = (over[i / 2] & h16) != 0;
             any |= __ballot(bad) ? 1u << i : 0u;
 #pragma unroll
-            for (int e = 0; e < NE; ++e) w[e][i / 2] &= bad ? ~half : ~0u;
+            for (int e = 0; e < NE; ++e) vs_now[e][i / 2] &= bad ? ~h16 : ~0u;
           }
         }
-        if (lane == 0) lds_bad[buf][wave] = any;
+        if (lane == 0) lds_bad[turn & 3][wave] = any;
       }
+    };
+    const auto decode_v = [&](int turn) {
 #pragma unroll
       for (int e = 0; e < NE; ++e) {
         f16x2_t vs[4], vs24[4];
@@ -1359,20 +1430,20 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
         for (int i = 0; i < 4; ++i) {
           const int i0 = value_at<FMT>(2 * i), i1 = value_at<FMT>(2 * i + 1);
           vs[i] = f16x2_t{
-              (_Float16)((i0 & 1) ? bf16_hi(w[e][i0 / 2]) : bf16_lo(w[e][i0 / 2])),
-              (_Float16)((i1 & 1) ? bf16_hi(w[e][i1 / 2]) : bf16_lo(w[e][i1 / 2]))};
+              (_Float16)((i0 & 1) ? bf16_hi(vs_now[e][i0 / 2]) : bf16_lo(vs_now[e][i0 / 2])),
+              (_Float16)((i1 & 1) ? bf16_hi(vs_now[e][i1 / 2]) : bf16_lo(vs_now[e][i1 / 2]))};
           vs24[i] = vs[i] * (f16x2_t){(_Float16)-24.0f, (_Float16)-24.0f};
         }
 #pragma unroll
         for (int i = 2 * e; i < N && i < 2 * e + 2; ++i)
-          lds_v[buf][map.blk][map.vd + v_step(i)] =
+          lds_v[turn & 1][map.blk][map.vd + v_step(i)] =
               __builtin_bit_cast(uint4, decode_f16<FMT>(st.v[i], vs, vs24));
       }
     };
 
     if (n_turns > 0) {
       load_pages(s0);
-      load(s0 + (wave >> 2));
+      tile_load_k<D>(a.w, codes_at(0), L, map, st);
     }
     f16x8_t q[D / 16];
     int pos;
@@ -1395,65 +1466,95 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
         }
       }
     }
-    f32x16_t o[NJ];
+    f32x16_t o[NJ], sc[NU];
+    f16x8_t p[HV == 2 ? 1 : 4];
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[j][i] = 0.0f;
     float m = -FLT_MAX, l = 0.0f;  // m: of the scores before scaling
-    if (n_turns > 0) decode(0, place_at(s0 + (wave >> 2)));
-    if (n_turns > 1) load(s0 + 2 + (wave >> 2));
-    __syncthreads();
-    for (int turn = 0; turn < n_turns; ++turn) {
-      const int buf = turn & 1, step = s0 + 2 * turn;
-      const int ta = place_at(step), tb = step + 1 < last ? place_at(step + 1) : 0x40000000;
-      // the next turn's place, before its pages may be replaced
-      const int t_next = turn + 1 < n_turns && step + 2 + (wave >> 2) < last
-                             ? place_at(step + 2 + (wave >> 2)) : 0x40000000;
-      const bool seen_a = ta <= w_hi, seen_b = tb <= w_hi;
-      const bool work = busy && (seen_a || seen_b);
-      f32x16_t sc[2];
-      if (work) tile_scores<D>(&lds_k[buf][h][k_tok], q, sc);
-      if (turn + 1 < n_turns) {
-        decode(buf ^ 1, t_next);
-        if (turn + 2 < n_turns) {
-          const int s2 = step + 4 + (wave >> 2);
-          if (step + 6 > page_base + 64) load_pages(step + 2);
-          load(s2);
-        }
+    if (n_turns > 0) {
+      // K of turn k and V of the turn before from their codes to LDS, and the next codes' loads
+      const auto decode_turn = [&](int k) {
+        if (k > n_turns) return;
+        decode_v(k - 1);
+        if (k >= n_turns) return;
+        decode_k(k);
+        // (pages of the scores of turn k - 2 at the earliest, K of turn k + 1 at the latest)
+        if (s0 + 2 * k + 4 > page_base + 64) load_pages(s0 + 2 * max(k - 2, 0));
+        tile_load_v<D>(codes_at(k), L, map, st);
+        if (k + 1 < n_turns) tile_load_k<D>(a.w, codes_at(k + 1), L, map, st);
+      };
+      const auto values = [&](int turn) {
+        tile_values<D, NJ>(&lds_v[turn & 1][h][32 * NJ * half + q32], [&](int b) {
+          if constexpr (HV == 2) return __builtin_bit_cast(f16x8_t, lds_p[rows32][b][lane]);
+          else return p[b];
+        }, o);
+      };
+      decode_k(0);
+      tile_load_v<D>(codes_at(0), L, map, st);
+      if (n_turns > 1) tile_load_k<D>(a.w, codes_at(1), L, map, st);
+      __syncthreads();
+      if (group == 1) {  // half a turn behind group 0
+        decode_turn(1);
+        __syncthreads();
       }
-      if (work) {
-        if (edge_at(ta, t.p_lo, t.p_hi) || edge_at(tb, t.p_lo, t.p_hi)) {
+#pragma unroll 1
+      for (int turn = 0; turn < n_turns; ++turn) {
+        // phase M
+        __builtin_amdgcn_s_setprio(1);
+        if (turn > 0) values(turn - 1);
+        tile_scores<D, NU>(&lds_k[turn & 1][h][32 * half + k_tok], q, sc);
+        __builtin_amdgcn_s_setprio(0);
+        float mx;
+        {
+          int tu[NU];
+          bool edge = false;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int t0 = u ? tb : ta;
-            uint32_t bad = 0;
-            if (edge_at(t0, t.p_lo, t.p_hi))
+          for (int u = 0; u < NU; ++u) {
+            tu[u] = place_at(turn, HV == 2 ? half : u);
+            edge |= edge_at(tu[u], t.p_lo, t.p_hi);
+          }
+          if (edge) {
 #pragma unroll
-              for (int b = 0; b < 4; ++b) bad |= lds_bad[buf][4 * u + b] << (8 * b);
-            if (!edge_at(t0, w_lo, w_hi) && bad == 0) continue;
-            // against the constant offset of a register's position
-            const int to = pos - t0 - 8 * h, from = a.window > 0 ? to - a.window : -1000;
-            const int first = a.sinks - t0 - 8 * h;
+            for (int u = 0; u < NU; ++u) {
+              uint32_t bad = 0;
+              if (edge_at(tu[u], t.p_lo, t.p_hi))
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int at = 16 * (i >> 3) + (i & 7);
-              const bool seen = at <= to && (at > from || at < first);
-              sc[u][i] = seen ? sc[u][i] : -INFINITY;
-            }
-            if (bad) {
-              const uint32_t mine = bad >> (8 * h);
+                for (int b = 0; b < 4; ++b)
+                  bad |= lds_bad[turn & 3][4 * (HV == 2 ? half : u) + b] << (8 * b);
+              if (!edge_at(tu[u], w_lo, w_hi) && bad == 0) continue;
+              // against the constant offset of a register's position
+              const int to = pos - tu[u] - 8 * h, from = a.window > 0 ? to - a.window : -1000;
+              const int first = a.sinks - tu[u] - 8 * h;
 #pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if ((mine >> (16 * (i >> 3) + (i & 7))) & 1 && sc[u][i] != -INFINITY) sc[u][i] = NAN;
+              for (int i = 0; i < 16; ++i) {
+                const int at = 16 * (i >> 3) + (i & 7);
+                const bool seen = at <= to && (at > from || at < first);
+                sc[u][i] = seen ? sc[u][i] : -INFINITY;
+              }
+              if (bad) {
+                const uint32_t mine = bad >> (8 * h);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  if ((mine >> (16 * (i >> 3) + (i & 7))) & 1 && sc[u][i] != -INFINITY)
+                    sc[u][i] = NAN;
+              }
             }
           }
-        }
-        float mx = fmaxf(sc[0][0], sc[1][0]);
+          mx = fmaxf(sc[0][0], sc[NU - 1][0]);
 #pragma unroll
-        for (int i = 1; i < 16; ++i) mx = fmaxf(fmaxf(mx, sc[0][i]), sc[1][i]);
-        if (__ballot(mx > m + move_by)) {
+          for (int i = 1; i < 16; ++i) mx = fmaxf(fmaxf(mx, sc[0][i]), sc[NU - 1][i]);
+        }
+        if constexpr (HV == 2) {
           mx = fmaxf(mx, __shfl_xor(mx, 32));
+          if (h == 0) lds_m[rows32][half][q32] = mx;
+        }
+        __syncthreads();
+        // phase A
+        if constexpr (HV == 2) mx = fmaxf(mx, lds_m[rows32][half ^ 1][q32]);
+        if (__ballot(mx > m + move_by)) {
+          if constexpr (HV == 1) mx = fmaxf(mx, __shfl_xor(mx, 32));
           mx = fmaxf(mx, m);
           const float f = __builtin_amdgcn_exp2f((m - mx) * c);
           m = mx;
@@ -1461,14 +1562,38 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
 #pragma unroll
           for (int j = 0; j < NJ; ++j) o[j] *= f;
         }
-        tile_values<D, FMT>(&lds_v[buf][h][q32], sc, c, P_SHIFT - fmaxf(m * c, -FLT_MAX), l, o);
+        const float ref = P_SHIFT - fmaxf(m * c, -FLT_MAX);
+#pragma unroll
+        for (int b = 0; b < 2 * NU; ++b) {  // 16 positions
+          float e[8];
+          f16x8_t w;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            e[i] = __builtin_amdgcn_exp2f(fmaf(sc[b >> 1][8 * (b & 1) + i], c, ref));
+          l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = (_Float16)e[value_at<FMT>(i)];
+          if constexpr (HV == 2)
+            lds_p[rows32][2 * half + b][lane] = __builtin_bit_cast(uint4, w);
+          else
+            p[b] = w;
+        }
+        decode_turn(turn + 1 + group);
+        __syncthreads();
       }
-      __syncthreads();
+      values(n_turns - 1);
+      if (group == 0) __syncthreads();
     }
 
     l += __shfl_xor(l, 32);
+    if constexpr (HV == 2) {
+      if (h == 0) lds_m[rows32][half][q32] = l;
+      __syncthreads();
+      l = lds_m[rows32][0][q32] + lds_m[rows32][1][q32];
+    }
     const float m2 = l != 0.0f ? m * c : -FLT_MAX;  // in powers of 2, as the other kernel's
     const int row = my0 + q32, place = 2 * (part0 + part) + (s0 == 0);
+    const int d0 = 32 * NJ * half + 4 * h;
     if (row < t.n_rho) {
       if (whole) {
         const float inv = row_inv(l);
@@ -1476,18 +1601,18 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
           for (int i = 0; i < 16; i += 4)
-            store_out4(a, t, D, row, 32 * j + 2 * i + 4 * h,
+            store_out4(a, t, D, row, d0 + 32 * j + 2 * i,
                        make_float4(o[j][i], o[j][i + 1], o[j][i + 2], o[j][i + 3]), inv);
-        if (h == 0) store_lse(a, t, row, m2, l);
+        if (d0 == 0) store_lse(a, t, row, m2, l);
       } else {
         const __amdgpu_buffer_rsrc_t pr = part_rsrc(a.part);
 #pragma unroll
         for (int j = 0; j < NJ; ++j)
 #pragma unroll
           for (int i = 0; i < 16; i += 4)
-            st4_agent(pr, place * SIZE + row * D + 32 * j + 2 * i + 4 * h,
+            st4_agent(pr, place * SIZE + row * D + d0 + 32 * j + 2 * i,
                       make_float4(o[j][i], o[j][i + 1], o[j][i + 2], o[j][i + 3]));
-        if (h == 0) {
+        if (d0 == 0) {
           st_sc1(a.part, (size_t)place * SIZE + R * D + row, m2);
           st_sc1(a.part, (size_t)place * SIZE + R * D + R + row, l);
         }
@@ -1497,51 +1622,7 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
     if (!whole) {
       const int first = spot.start / per, n = (spot.start + spot.steps - 1) / per - first + 1;
       if (last_arriver(a.counters + part0 + first, (unsigned)n, &lds_flag)) {
-        // every thread keeps D / 8 columns of 4 rows apart: 16 bytes at a time, part by part
-        const __amdgpu_buffer_rsrc_t pr = part_rsrc(a.part);
-        constexpr int LR = D / 4, RS = TILE_THREADS / LR;  // lanes of a row, rows at once
-        for (int r0 = tid / LR; r0 < t.n_rho; r0 += 4 * RS) {
-          const int d = 4 * (tid % LR);
-          float mm[4], ll[4];
-          float4 oo[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            mm[u] = -FLT_MAX;
-            ll[u] = 0.0f;
-            oo[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          }
-          for (int k = 0; k < n; ++k) {
-            const int at = (2 * (part0 + first + k) + (k == 0)) * SIZE;
-            float4 v[4];
-            float pm[4], pl[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int rr = min(r0 + u * RS, t.n_rho - 1);
-              v[u] = ld4_agent(pr, at + rr * D + d);
-              pm[u] = __uint_as_float(
-                  __builtin_amdgcn_raw_buffer_load_b32(pr, (at + R * D + rr) * 4, 0, 16));
-              pl[u] = __uint_as_float(
-                  __builtin_amdgcn_raw_buffer_load_b32(pr, (at + R * D + R + rr) * 4, 0, 16));
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const float mx = fmaxf(mm[u], pm[u]);
-              const float f0 = __builtin_amdgcn_exp2f(mm[u] - mx), f = __builtin_amdgcn_exp2f(pm[u] - mx);
-              mm[u] = mx;
-              ll[u] = ll[u] * f0 + pl[u] * f;
-              oo[u].x = oo[u].x * f0 + v[u].x * f; oo[u].y = oo[u].y * f0 + v[u].y * f;
-              oo[u].z = oo[u].z * f0 + v[u].z * f; oo[u].w = oo[u].w * f0 + v[u].w * f;
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int rr = r0 + u * RS;
-            if (rr < t.n_rho) {
-              store_out4(a, t, D, rr, d, oo[u], row_inv(ll[u]));
-              if (d == 0) store_lse(a, t, rr, mm[u], ll[u]);
-            }
-          }
-        }
+        join_tiles<D, R>(a, t, part0, first, n, tid);
         if (tid == 0) st_cnt(a.counters + part0 + first, 0u);
       }
     }
@@ -1565,7 +1646,7 @@ hipError_t launch_rows(const Kv4RowsArgs& a, hipStream_t st) {
 template <int D, int FMT>
 hipError_t launch_attn(const Kv4AttnArgs& a, hipStream_t st) {
   const unsigned grid = (unsigned)a.w.Hkv * (a.part ? a.n_parts : a.n_slots);
-  if (a.nt == KV4_TILE_NT) {
+  if (a.nt == kv4_tile_nt(D)) {
     kv4_attn_tiles_kernel<D, FMT><<<grid, TILE_THREADS, 0, st>>>(a);
     return hipGetLastError();
   }
