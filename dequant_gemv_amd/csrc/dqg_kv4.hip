@@ -1155,33 +1155,45 @@ struct TileMap {
     vd = D == 64 ? lane : (lane >> 4) * 32 + (lane & 15);
   }
 };
+// A thread's byte offsets from a step's codes: its own are constant, the scales lie `scales` away.
 template <int D>
-__device__ __forceinline__ void tile_load_k(const Kv4Where& w, const Place& p, const Layout<D>& L,
-                                            const TileMap<D>& m, TileStage<D>& x) {
-  const int tok = m.tok & (KV4_STEP - 1), blk = m.blk & 3;
-  const uint32_t* k = reinterpret_cast<const uint32_t*>(p.codes + tok * (D / 2)) + m.kd;
-  if constexpr (D == 64) {
-    x.k[0] = k[0];
-  } else if constexpr (D == 128) {
-    const uint2 u = *reinterpret_cast<const uint2*>(k);
-    x.k[0] = u.x; x.k[1] = u.y;
-  } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(k);
-    x.k[0] = u.x; x.k[1] = u.y; x.k[2] = u.z; x.k[3] = u.w;
-  }
-  x.ks = *reinterpret_cast<const uint16_t*>(p.scales + L.ks +
-                                            2 * ((tok << L.n_shift) + ((8 * m.kd) >> w.group_shift)));
+struct TileOffsets {
+  uint32_t kc, vc, ks, vs[TileStage<D>::NE];
+  __device__ __forceinline__ TileOffsets(const Kv4Where& w, const Layout<D>& L, const TileMap<D>& m) {
+    const int tok = m.tok & (KV4_STEP - 1), blk = m.blk & 3;
+    kc = tok * (D / 2) + 4 * m.kd;
+    vc = L.vc + (blk * D + m.vd) * 4;
+    ks = L.ks + 2 * ((tok << L.n_shift) + ((8 * m.kd) >> w.group_shift));
 #pragma unroll
-  for (int e = 0; e < TileStage<D>::NE; ++e)
-    x.vs[e] = *reinterpret_cast<const uint4*>(
-        p.scales + L.vs + 16 * ((blk << L.n_shift) + ((m.vd + 128 * e) >> w.group_shift)));
+    for (int e = 0; e < TileStage<D>::NE; ++e)
+      vs[e] = L.vs + 16 * ((blk << L.n_shift) + ((m.vd + 128 * e) >> w.group_shift));
+  }
+};
+template <class T>
+__device__ __forceinline__ T load_at(const uint8_t* base, uint32_t off) {
+  return *reinterpret_cast<const T*>(base + off);
 }
 template <int D>
-__device__ __forceinline__ void tile_load_v(const Place& p, const Layout<D>& L, const TileMap<D>& m,
-                                            TileStage<D>& x) {
-  const uint32_t* v = reinterpret_cast<const uint32_t*>(p.codes + L.vc) + (m.blk & 3) * D + m.vd;
+__device__ __forceinline__ void tile_load_k(const uint8_t* codes, uint32_t scales,
+                                            const TileOffsets<D>& off, TileStage<D>& x) {
+  if constexpr (D == 64) {
+    x.k[0] = load_at<uint32_t>(codes, off.kc);
+  } else if constexpr (D == 128) {
+    const uint2 u = load_at<uint2>(codes, off.kc);
+    x.k[0] = u.x; x.k[1] = u.y;
+  } else {
+    const uint4 u = load_at<uint4>(codes, off.kc);
+    x.k[0] = u.x; x.k[1] = u.y; x.k[2] = u.z; x.k[3] = u.w;
+  }
+  x.ks = load_at<uint16_t>(codes, off.ks + scales);
 #pragma unroll
-  for (int i = 0; i < TileStage<D>::N; ++i) x.v[i] = v[v_step(i)];
+  for (int e = 0; e < TileStage<D>::NE; ++e) x.vs[e] = load_at<uint4>(codes, off.vs[e] + scales);
+}
+template <int D>
+__device__ __forceinline__ void tile_load_v(const uint8_t* codes, const TileOffsets<D>& off,
+                                            TileStage<D>& x) {
+#pragma unroll
+  for (int i = 0; i < TileStage<D>::N; ++i) x.v[i] = load_at<uint32_t>(codes, off.vc + 4 * v_step(i));
 }
 
 // Keeps the order of what is written on both sides: left alone, the compiler reads one operand from
@@ -1328,6 +1340,7 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
   }
   const Layout<D> L(a.w);
   const TileMap<D> map(tid);
+  const TileOffsets<D> off(a.w, L, map);
   // row m of an A operand of K -> its position within 32
   const int k_tok = 16 * (q32 >> 4) + 8 * ((q32 >> 2) & 1) + 4 * ((q32 >> 3) & 1) + (q32 & 3);
   // the sign of the scale goes to Q; 1e-30 stands for a scale of 0 (equal weights all the same)
@@ -1355,33 +1368,38 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
     const int p_first = t.s.len - t.s.n;
     const int w_lo = p_first + row_of(a, t.rho0 + min(my0, t.n_rho - 1));
     const int w_hi = p_first + row_of(a, t.rho0 + min(my0 + 31, t.n_rho - 1));
-    // pages of 64 steps from page_base on, one a lane; -1: no such step, or no such page
-    int pages = -1, page_base = s0;
-    const auto load_pages = [&](int from) {
-      page_base = from;
-      const int step = min(from + lane, last - 1);
-      pages = a.w.table[(int64_t)t.b * a.w.max_pages + (position_of(t, step) >> a.w.page_shift)];
-      if (pages < 0 || pages >= a.w.num_pages) {
-        if (from + lane < last) report(a.w.status, ST_PAGE);
-        pages = -1;
-      }
-      if (from + lane >= last) pages = -1;
-    };
-    // the place of the u-th half of a turn
-    const auto place_at = [&](int turn, int u) {
-      const int step = s0 + 2 * turn + u;
-      if (step >= last || __builtin_amdgcn_readlane(pages, step - page_base) < 0) return NOWHERE;
-      return position_of(t, step);
-    };
-    // where a thread reads its codes of a turn (what is not there is read from some page: hidden)
-    const auto codes_at = [&](int turn) {
-      const int step = min(s0 + 2 * turn + group, last - 1);
-      const int page = __builtin_amdgcn_readlane(pages, step - page_base);
-      return place_of<D>(a.w, head, max(page, 0), position_of(t, step));
-    };
     const auto edge_at = [&](int t0, int lo, int hi) {
       return t0 + KV4_STEP - 1 > lo ||
              (a.window > 0 && t0 <= hi - a.window && t0 + KV4_STEP > a.sinks);
+    };
+    // 64 steps from list0 on, one a lane: position, offset of the codes in the cache, how far the
+    // scales are from there; and which steps some row of the workgroup, or of the wavefront,
+    // does not see whole.  A step that is not there is read somewhere and seen nowhere.
+    int list0 = s0, l_pos = NOWHERE, l_scales = 0;
+    int64_t l_codes = 0;
+    uint64_t edges = 0, my_edges = 0;
+    const auto load_list = [&](int from) {
+      list0 = from;
+      const int at = position_of(t, min(from + lane, last - 1));
+      int page = a.w.table[(int64_t)t.b * a.w.max_pages + (at >> a.w.page_shift)];
+      const bool there = page >= 0 && page < a.w.num_pages, mine = from + lane < last;
+      if (!there && mine) report(a.w.status, ST_PAGE);
+      page = there ? page : 0;
+      l_pos = there && mine ? at : NOWHERE;
+      const int in_page = at & ((1 << a.w.page_shift) - 1);
+      l_codes = page * a.w.page_bytes + (int64_t)head * a.w.head_bytes + in_page * (D / 2);
+      l_scales = ((in_page << L.n_shift) << 1) - in_page * (D / 2);
+      edges = __ballot(edge_at(l_pos, t.p_lo, t.p_hi));
+      my_edges = __ballot(edge_at(l_pos, w_lo, w_hi));
+    };
+    // where the thread reads its codes of a turn
+    const uint8_t* codes = a.w.cache;
+    uint32_t scales = 0;
+    const auto go_to = [&](int turn) {
+      const int i = s0 + 2 * turn + group - list0;
+      codes = a.w.cache + (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(l_codes >> 32), i) << 32) |
+                                    (uint32_t)__builtin_amdgcn_readlane((int)l_codes, i));
+      scales = (uint32_t)__builtin_amdgcn_readlane(l_scales, i);
     };
     TileStage<D> st;
     uint32_t vs_now[NE][4];  // V scales of the turn whose V is decoded next
@@ -1398,7 +1416,7 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
         vs_now[e][0] = st.vs[e].x; vs_now[e][1] = st.vs[e].y;
         vs_now[e][2] = st.vs[e].z; vs_now[e][3] = st.vs[e].w;
       }
-      if (edge_at(place_at(turn, group), t.p_lo, t.p_hi)) {
+      if ((edges >> (s0 + 2 * turn + group - list0)) & 1) {
         // scales that fp16 cannot take: cleared, and the rows that see them are told.  (In a step
         // that all rows see whole they do their damage by themselves.)
         uint32_t over[4], any_over = 0, any = 0;
@@ -1442,8 +1460,9 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
     };
 
     if (n_turns > 0) {
-      load_pages(s0);
-      tile_load_k<D>(a.w, codes_at(0), L, map, st);
+      load_list(s0);
+      go_to(0);
+      tile_load_k<D>(codes, scales, off, st);
     }
     f16x8_t q[D / 16];
     int pos;
@@ -1480,10 +1499,12 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
         decode_v(k - 1);
         if (k >= n_turns) return;
         decode_k(k);
-        // (pages of the scores of turn k - 2 at the earliest, K of turn k + 1 at the latest)
-        if (s0 + 2 * k + 4 > page_base + 64) load_pages(s0 + 2 * max(k - 2, 0));
-        tile_load_v<D>(codes_at(k), L, map, st);
-        if (k + 1 < n_turns) tile_load_k<D>(a.w, codes_at(k + 1), L, map, st);
+        tile_load_v<D>(codes, off, st);
+        if (k + 1 >= n_turns) return;
+        // (the list has the scores of turn k - 2 at the earliest, K of turn k + 1 at the latest)
+        if (s0 + 2 * k + 4 > list0 + 64) load_list(s0 + 2 * max(k - 2, 0));
+        go_to(k + 1);
+        tile_load_k<D>(codes, scales, off, st);
       };
       const auto values = [&](int turn) {
         tile_values<D, NJ>(&lds_v[turn & 1][h][32 * NJ * half + q32], [&](int b) {
@@ -1492,8 +1513,11 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
         }, o);
       };
       decode_k(0);
-      tile_load_v<D>(codes_at(0), L, map, st);
-      if (n_turns > 1) tile_load_k<D>(a.w, codes_at(1), L, map, st);
+      tile_load_v<D>(codes, off, st);
+      if (n_turns > 1) {
+        go_to(1);
+        tile_load_k<D>(codes, scales, off, st);
+      }
       __syncthreads();
       if (group == 1) {  // half a turn behind group 0
         decode_turn(1);
@@ -1508,25 +1532,21 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
         __builtin_amdgcn_s_setprio(0);
         float mx;
         {
-          int tu[NU];
-          bool edge = false;
-#pragma unroll
-          for (int u = 0; u < NU; ++u) {
-            tu[u] = place_at(turn, HV == 2 ? half : u);
-            edge |= edge_at(tu[u], t.p_lo, t.p_hi);
-          }
-          if (edge) {
+          const int i0 = s0 + 2 * turn + (HV == 2 ? half : 0) - list0;
+          constexpr uint64_t UM = (1u << NU) - 1;
+          if ((edges >> i0) & UM) {
 #pragma unroll
             for (int u = 0; u < NU; ++u) {
               uint32_t bad = 0;
-              if (edge_at(tu[u], t.p_lo, t.p_hi))
+              if ((edges >> (i0 + u)) & 1)
 #pragma unroll
                 for (int b = 0; b < 4; ++b)
                   bad |= lds_bad[turn & 3][4 * (HV == 2 ? half : u) + b] << (8 * b);
-              if (!edge_at(tu[u], w_lo, w_hi) && bad == 0) continue;
+              if (!((my_edges >> (i0 + u)) & 1) && bad == 0) continue;
+              const int t0 = __builtin_amdgcn_readlane(l_pos, i0 + u);
               // against the constant offset of a register's position
-              const int to = pos - tu[u] - 8 * h, from = a.window > 0 ? to - a.window : -1000;
-              const int first = a.sinks - tu[u] - 8 * h;
+              const int to = pos - t0 - 8 * h, from = a.window > 0 ? to - a.window : -1000;
+              const int first = a.sinks - t0 - 8 * h;
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
                 const int at = 16 * (i >> 3) + (i & 7);

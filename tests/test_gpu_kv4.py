@@ -217,14 +217,15 @@ def run_attention(c, q, cu, lens, table, fmt, G, page, scale=None, window=0, sin
     assert torch.equal(lo[n:].view(torch.int32), before_lse[n:].view(torch.int32))
     bound, lse_bound = U.attention_bounds((want, lse), slack, D)
     err = np.abs(got[:n] - want[:n])
-    assert np.all(np.isfinite(got[:n]))
+    assert int((~np.isfinite(got[:n])).sum()) == 0
     assert np.all(err <= bound[:n]), (
         f"{int((err > bound[:n]).sum())} of {err.size} outputs out of bounds, worst "
         f"{float((err / bound[:n]).max())} x at {np.unravel_index(int((err / bound[:n]).argmax()), err.shape)}")
     empty = np.isneginf(lse[:n])
     assert np.array_equal(np.isneginf(got_lse[:n]), empty)
-    assert np.all(np.abs(np.where(empty, 0, got_lse[:n]) - np.where(empty, 0, lse[:n]))
-                  <= np.where(empty, 0, lse_bound[:n]))
+    off = np.abs(np.where(empty, 0, got_lse[:n]) - np.where(empty, 0, lse[:n]))
+    over = off > np.where(empty, 0, lse_bound[:n])
+    assert not over.any(), f"{int(over.sum())} lse out of bounds, worst off by {float(off.max())}"
 
 
 def attention_case(rows, lens, D, H, r, fmt, G, page, seed=0, q_scale=1.0, **kw):
