@@ -770,11 +770,14 @@ int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32
   // one 16-row tile holds a token's heads; two share the decoded keys and values
   const int nt = (long long)rows * a.r <= 16 || D > 128 ? 1 : 2;
   if (rows <= few) return launch(nt, 0, INT_MAX, kKv4MinSteps);
-  if (B > 1 && few > 0) {  // sequences of few rows among those of many
+  // sequences of few rows may stand among those of many: they get a launch of their own where the
+  // average sequence does not fill a tile (a launch that finds none costs 4 us)
+  const bool mixed = few > 0 && B > 1 && (long long)T * a.r < (long long)B * 16 * dqg::kv4_tile_nt(D);
+  if (mixed) {
     rc = launch(nt, 0, few, kKv4MinSteps);
     if (rc != DQG_OK) return rc;
   }
-  return launch(dqg::kv4_tile_nt(D), B > 1 ? few : 0, INT_MAX, kKv4MinTileSteps);
+  return launch(dqg::kv4_tile_nt(D), mixed ? few : 0, INT_MAX, kKv4MinTileSteps);
 }
 
 int packed_dequant_f32(const uint8_t* w, const uint16_t* s, int K, int N, int group,

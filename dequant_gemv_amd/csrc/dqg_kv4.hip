@@ -1108,15 +1108,17 @@ __global__ __launch_bounds__(64 * ROWS_WAVES, 2) void kv4_attn_rows_kernel(Kv4At
 // half of a turn's positions for S and half of the columns of O, whose sums would not fit
 // otherwise, and they trade row maxima and weights through LDS.
 //
-// A turn of a wavefront is two phases, a barrier behind each: M, the matrix instructions (S of
-// this turn, O of the turn before), and A, the arithmetic (weights of this turn, decoding).
-// Wavefronts 0-3 and 4-7, one of each on every SIMD, are in opposite phases, so that the matrix
-// cores and the vector ALUs work at the same time.
-// Slot 2 t (between two barriers) is phase M of turn t for group 0 and phase A of turn t - 1 for
-// group 1, slot 2 t + 1 the other way round; the phases A of both slots decode K of turn t + 1 and V
-// of turn t, each thread its share.  (K of turn t + 1 takes the place of turn t - 1's, last read
-// in slot 2 t - 1, and is first read in slot 2 t + 2; V of turn t that of turn t - 2's, last read in
-// slot 2 t - 1, first read in slot 2 t + 2.)
+// Wavefronts 0-3 (group 0) and 4-7 (group 1), one of each on every SIMD, do a turn's work in
+// different orders, so that one has matrix instructions while the other has arithmetic.
+// D <= 128, one barrier a turn (two buffers of K and of V): group 0 takes scores, weights, outputs,
+// decoding of the next turn; group 1 starts with the decoding.
+// D = 256: two phases with a barrier behind each: M, the matrix instructions (S of this turn, O of
+// the turn before), and A, the arithmetic (weights of this turn, decoding).  Slot 2 t (between two
+// barriers) is phase M of turn t for group 0 and phase A of turn t - 1 for group 1, slot 2 t + 1 the
+// other way round; the phases A of both slots decode K of turn t + 1 and V of turn t, each thread
+// its share.  (K of turn t + 1 takes the place of turn t - 1's, last read in slot 2 t - 1, and is
+// first read in slot 2 t + 2; V of turn t that of turn t - 2's, last read in slot 2 t - 1, first
+// read in slot 2 t + 2.)
 constexpr int TILE_POS = 64, TILE_THREADS = 512, K_STRIDE = TILE_POS + 1;
 __host__ __device__ constexpr int tile_halves(int D) { return D > 128 ? 2 : 1; }
 __host__ __device__ constexpr int tile_rows(int D) { return 16 * kv4_tile_nt(D); }
@@ -1486,13 +1488,100 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
       }
     }
     f32x16_t o[NJ], sc[NU];
-    f16x8_t p[HV == 2 ? 1 : 4];
 #pragma unroll
     for (int j = 0; j < NJ; ++j)
 #pragma unroll
       for (int i = 0; i < 16; ++i) o[j][i] = 0.0f;
     float m = -FLT_MAX, l = 0.0f;  // m: of the scores before scaling
-    if (n_turns > 0) {
+    // hides what the rows do not see of a turn's scores; the lane's largest score
+    const auto mask_scores = [&](int turn) {
+      float mx;
+                const int i0 = s0 + 2 * turn + (HV == 2 ? half : 0) - list0;
+                constexpr uint64_t UM = (1u << NU) - 1;
+                if ((edges >> i0) & UM) {
+      #pragma unroll
+                  for (int u = 0; u < NU; ++u) {
+                    uint32_t bad = 0;
+                    if ((edges >> (i0 + u)) & 1)
+      #pragma unroll
+                      for (int b = 0; b < 4; ++b)
+                        bad |= lds_bad[turn & 3][4 * (HV == 2 ? half : u) + b] << (8 * b);
+                    if (!((my_edges >> (i0 + u)) & 1) && bad == 0) continue;
+                    const int t0 = __builtin_amdgcn_readlane(l_pos, i0 + u);
+                    // against the constant offset of a register's position
+                    const int to = pos - t0 - 8 * h, from = a.window > 0 ? to - a.window : -1000;
+                    const int first = a.sinks - t0 - 8 * h;
+      #pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                      const int at = 16 * (i >> 3) + (i & 7);
+                      const bool seen = at <= to && (at > from || at < first);
+                      sc[u][i] = seen ? sc[u][i] : -INFINITY;
+                    }
+                    if (bad) {
+                      const uint32_t mine = bad >> (8 * h);
+      #pragma unroll
+                      for (int i = 0; i < 16; ++i)
+                        if ((mine >> (16 * (i >> 3) + (i & 7))) & 1 && sc[u][i] != -INFINITY)
+                          sc[u][i] = NAN;
+                    }
+                  }
+                }
+                mx = fmaxf(sc[0][0], sc[NU - 1][0]);
+      #pragma unroll
+                for (int i = 1; i < 16; ++i) mx = fmaxf(fmaxf(mx, sc[0][i]), sc[NU - 1][i]);
+      return mx;
+    };
+    const auto move_reference = [&](float mx) {  // mx: of the row
+      if (__ballot(mx > m + move_by)) {
+        if constexpr (HV == 1) mx = fmaxf(mx, __shfl_xor(mx, 32));
+        mx = fmaxf(mx, m);
+        const float f = __builtin_amdgcn_exp2f((m - mx) * c);
+        m = mx;
+        l *= f;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) o[j] *= f;
+      }
+      return P_SHIFT - fmaxf(m * c, -FLT_MAX);
+    };
+    // the weights of the b-th 16 positions of the wavefront
+    const auto weights = [&](int b, float ref) {
+      float e[8];
+      f16x8_t w;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        e[i] = __builtin_amdgcn_exp2f(fmaf(sc[b >> 1][8 * (b & 1) + i], c, ref));
+      l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = (_Float16)e[value_at<FMT>(i)];
+      return w;
+    };
+    if constexpr (HV == 1) {
+      if (n_turns > 0) {
+        const auto decode_next = [&](int k) {
+          if (k >= n_turns) return;
+          decode_k(k);
+          decode_v(k);
+          if (k + 1 >= n_turns) return;
+          // (the list has the scores of turn k - 1 and K of turn k + 1)
+          if (s0 + 2 * k + 4 > list0 + 64) load_list(s0 + 2 * (k - 1));
+          go_to(k + 1);
+          tile_load_k<D>(codes, scales, off, st);
+          tile_load_v<D>(codes, off, st);
+        };
+        tile_load_v<D>(codes, off, st);
+        decode_next(0);
+        __syncthreads();
+#pragma unroll 1
+        for (int turn = 0; turn < n_turns; ++turn) {
+          if (group == 1) decode_next(turn + 1);
+          tile_scores<D, NU>(&lds_k[turn & 1][h][k_tok], q, sc);
+          const float ref = move_reference(mask_scores(turn));
+          tile_values<D, NJ>(&lds_v[turn & 1][h][q32], [&](int b) { return weights(b, ref); }, o);
+          if (group == 0) decode_next(turn + 1);
+          __syncthreads();
+        }
+      }
+    } else if (n_turns > 0) {
       // K of turn k and V of the turn before from their codes to LDS, and the next codes' loads
       const auto decode_turn = [&](int k) {
         if (k > n_turns) return;
@@ -1508,8 +1597,7 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
       };
       const auto values = [&](int turn) {
         tile_values<D, NJ>(&lds_v[turn & 1][h][32 * NJ * half + q32], [&](int b) {
-          if constexpr (HV == 2) return __builtin_bit_cast(f16x8_t, lds_p[rows32][b][lane]);
-          else return p[b];
+          return __builtin_bit_cast(f16x8_t, lds_p[rows32][b][lane]);
         }, o);
       };
       decode_k(0);
@@ -1530,74 +1618,16 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
         if (turn > 0) values(turn - 1);
         tile_scores<D, NU>(&lds_k[turn & 1][h][32 * half + k_tok], q, sc);
         __builtin_amdgcn_s_setprio(0);
-        float mx;
-        {
-          const int i0 = s0 + 2 * turn + (HV == 2 ? half : 0) - list0;
-          constexpr uint64_t UM = (1u << NU) - 1;
-          if ((edges >> i0) & UM) {
-#pragma unroll
-            for (int u = 0; u < NU; ++u) {
-              uint32_t bad = 0;
-              if ((edges >> (i0 + u)) & 1)
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-                  bad |= lds_bad[turn & 3][4 * (HV == 2 ? half : u) + b] << (8 * b);
-              if (!((my_edges >> (i0 + u)) & 1) && bad == 0) continue;
-              const int t0 = __builtin_amdgcn_readlane(l_pos, i0 + u);
-              // against the constant offset of a register's position
-              const int to = pos - t0 - 8 * h, from = a.window > 0 ? to - a.window : -1000;
-              const int first = a.sinks - t0 - 8 * h;
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int at = 16 * (i >> 3) + (i & 7);
-                const bool seen = at <= to && (at > from || at < first);
-                sc[u][i] = seen ? sc[u][i] : -INFINITY;
-              }
-              if (bad) {
-                const uint32_t mine = bad >> (8 * h);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  if ((mine >> (16 * (i >> 3) + (i & 7))) & 1 && sc[u][i] != -INFINITY)
-                    sc[u][i] = NAN;
-              }
-            }
-          }
-          mx = fmaxf(sc[0][0], sc[NU - 1][0]);
-#pragma unroll
-          for (int i = 1; i < 16; ++i) mx = fmaxf(fmaxf(mx, sc[0][i]), sc[NU - 1][i]);
-        }
-        if constexpr (HV == 2) {
-          mx = fmaxf(mx, __shfl_xor(mx, 32));
-          if (h == 0) lds_m[rows32][half][q32] = mx;
-        }
+        float mx = mask_scores(turn);
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        if (h == 0) lds_m[rows32][half][q32] = mx;
         __syncthreads();
         // phase A
-        if constexpr (HV == 2) mx = fmaxf(mx, lds_m[rows32][half ^ 1][q32]);
-        if (__ballot(mx > m + move_by)) {
-          if constexpr (HV == 1) mx = fmaxf(mx, __shfl_xor(mx, 32));
-          mx = fmaxf(mx, m);
-          const float f = __builtin_amdgcn_exp2f((m - mx) * c);
-          m = mx;
-          l *= f;
+        mx = fmaxf(mx, lds_m[rows32][half ^ 1][q32]);
+        const float ref = move_reference(mx);
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) o[j] *= f;
-        }
-        const float ref = P_SHIFT - fmaxf(m * c, -FLT_MAX);
-#pragma unroll
-        for (int b = 0; b < 2 * NU; ++b) {  // 16 positions
-          float e[8];
-          f16x8_t w;
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            e[i] = __builtin_amdgcn_exp2f(fmaf(sc[b >> 1][8 * (b & 1) + i], c, ref));
-          l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = (_Float16)e[value_at<FMT>(i)];
-          if constexpr (HV == 2)
-            lds_p[rows32][2 * half + b][lane] = __builtin_bit_cast(uint4, w);
-          else
-            p[b] = w;
-        }
+        for (int b = 0; b < 2 * NU; ++b)
+          lds_p[rows32][2 * half + b][lane] = __builtin_bit_cast(uint4, weights(b, ref));
         decode_turn(turn + 1 + group);
         __syncthreads();
       }
