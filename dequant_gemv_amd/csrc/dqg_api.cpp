@@ -303,11 +303,10 @@ bool gemv_sizes_ok(int T, int K, int N, int group) {
 constexpr int kKv4MaxT = 1 << 22;
 constexpr int kKv4MaxB = 65536;
 constexpr int kKv4MaxHeads = 1024;
-// Workgroups of the attention kernel that run at once, one of 8 wavefronts a compute unit: the line
-// of steps is cut into as many parts.
+// Workgroups of the attention kernels that run at once, one of 8 wavefronts a compute unit.
 constexpr int kKv4Resident = 256;
-constexpr int kKv4MinSteps = 8;       // steps of a part, at least: one for each wavefront
-constexpr int kKv4MinTileSteps = 32;  // the same of the kernel for many rows
+constexpr int kKv4MinSteps = 8;       // steps of a piece, at least: one for each wavefront
+constexpr int kKv4MinTileSteps = 16;  // the same of the kernel for many rows: 8 turns
 // rows (query rows times the query heads of a kv head) of a sequence from which on it goes to the
 // kernel for many rows
 constexpr int kKv4FewRows = 32;
@@ -323,8 +322,9 @@ inline int log2_of(int v) { return 31 - __builtin_clz((unsigned)v); }
 
 // parts of a head's steps: as many as run at once
 int kv4_parts(int Hkv) { return std::max(kKv4Resident / Hkv, 1); }
-// [counters, one a part][partials, two a part]
-size_t kv4_counter_bytes() { return sizeof(unsigned) * std::max(kKv4Resident, kKv4MaxHeads); }
+// A tile that is cut has more than `per` steps and per >= (all steps) / parts, so there are at most
+// `parts` such tiles and 2 parts pieces of them: [counters][partials], 2 parts of each.
+size_t kv4_counter_bytes(int Hkv) { return up256(sizeof(unsigned) * 2 * Hkv * kv4_parts(Hkv)); }
 long long kv4_steps(long long positions) {
   return (positions + dqg::KV4_STEP - 1) / dqg::KV4_STEP;
 }
@@ -708,7 +708,7 @@ int kv4_read(uint16_t* k, uint16_t* v, int T, int64_t k_stride, int64_t v_stride
 size_t kv4_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int max_kv_len) {
   if (!kv4_attn_sizes_ok(T, B, Hq, Hkv, D) || max_kv_len < 1 || max_kv_len > (1 << 30)) return 0;
   if (max_kv_len <= kKv4MinSteps * dqg::KV4_STEP) return 0;
-  return up256(kv4_counter_bytes() + 2 * (size_t)Hkv * kv4_parts(Hkv) * sizeof(float) *
+  return up256(kv4_counter_bytes(Hkv) + 2 * (size_t)Hkv * kv4_parts(Hkv) * sizeof(float) *
                                          dqg::kv4_part_floats(dqg::kv4_tile_nt(D), D));
 }
 
@@ -752,19 +752,18 @@ int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32
     a.rows_over = over;
     a.rows_to = to;
     a.min_steps = min_steps;
-    a.n_slots = (int)((long long)T * a.r / R) + B;
-    const long long tiles =
-        Hkv * std::min<long long>(a.n_slots, (long long)B * (((long long)rows * a.r + R - 1) / R));
-    a.n_parts = (int)std::max(1LL, std::min<long long>(kv4_parts(Hkv), (tiles / Hkv * steps + min_steps - 1) /
-                                                                           min_steps));
-    // many-row tiles are cut only where they are too few to fill the GPU by themselves (two rounds);
-    // places on the line are 32-bit
-    const bool cut = workspace && (nt < dqg::kv4_tile_nt(D) || tiles < 2 * kKv4Resident) &&
-                     (long long)a.n_slots * (cap / dqg::KV4_STEP) < (1LL << 30);
+    // sum of ceil(n r / R) over the sequences; pieces are at most tiles + parts
+    const long long most = (long long)T * a.r / R + B;
+    const long long tiles = std::min(most, (long long)B * (((long long)rows * a.r + R - 1) / R));
+    // (hints may be wrong: any n_parts gives the right result)
+    a.n_parts = (int)std::max(1LL, std::min<long long>(kv4_parts(Hkv), (tiles * steps + min_steps - 1) / min_steps));
+    // places in a batch's steps are 32-bit
+    const bool cut = workspace && most * (cap / dqg::KV4_STEP) < (1LL << 30);
     a.counters = cut ? static_cast<unsigned*>(workspace) : nullptr;
-    a.part = cut ? reinterpret_cast<float*>(static_cast<char*>(workspace) + kv4_counter_bytes())
+    a.part = cut ? reinterpret_cast<float*>(static_cast<char*>(workspace) + kv4_counter_bytes(Hkv))
                  : nullptr;
-    if ((long long)a.n_slots * Hkv >= (1LL << 31)) return DQG_ERR_UNSUPPORTED;
+    a.n_groups = (int)(most + (cut ? a.n_parts : 0));
+    if ((long long)a.n_groups * Hkv >= (1LL << 31)) return DQG_ERR_UNSUPPORTED;
     return dqg::launch_kv4_attention(a, D, format, stream) == hipSuccess ? DQG_OK : DQG_ERR_HIP;
   };
   // one 16-row tile holds a token's heads; two share the decoded keys and values

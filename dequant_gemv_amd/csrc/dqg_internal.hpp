@@ -150,15 +150,16 @@ struct Kv4AttnArgs {
   int64_t q_stride, out_stride;
   uint16_t* out;
   float* lse;            // [T, Hq] or null
-  float* part;           // partial sums, two a part and head; null: tiles are not cut
-  unsigned* counters;    // [Hkv * n_parts], zero between calls
+  float* part;           // partial sums [Hkv][2 n_parts]; null: tiles are not cut
+  unsigned* counters;    // [Hkv][2 n_parts], zero between calls
   int Hq, r;             // query heads, and query heads per kv head
   uint32_t r_mul;        // division by r (see row_of)
   int r_shift;
   float scale;
   int window, sinks;
-  int n_slots, n_parts;  // row-tile slots; parts of a head's steps
-  int min_steps;         // steps of a part, at least
+  int n_parts;           // workgroups of a head that run at once
+  int n_groups;          // workgroups of a head: at least as many as pieces
+  int min_steps;         // steps of a piece, at least
   int nt;                // 16-row tiles per workgroup: 1, 2 or kv4_tile_nt(D)
   int rows_over, rows_to;  // the launch takes sequences of more rows than the one, up to the other
 };

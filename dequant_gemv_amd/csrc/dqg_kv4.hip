@@ -442,15 +442,6 @@ __device__ __forceinline__ bool takes_seq(const Kv4AttnArgs& a, const Seq& s) {
 __device__ __forceinline__ int position_of(const Tile& t, int step) {
   return (step < t.sink_steps ? step : step - t.sink_steps + t.main0) * KV4_STEP;
 }
-// The tile of a slot: sequence b has floor(cu[b] r / R) + b .. as its first, which leaves room for
-// its ceil(n r / R) tiles.
-__device__ __forceinline__ bool tile_at(const Kv4AttnArgs& a, int slot, int head, int R, Tile& t) {
-  const int r = a.r;
-  const int b = seq_of_slot(a.w, slot, 1, [=](int c) { return (int)((int64_t)c * r / R); });
-  const Seq s = seq_at(a.w, b);
-  return takes_seq(a, s) && tile_of(a, s, b, slot - ((int)((int64_t)s.row0 * r / R) + b), head, R, t);
-}
-
 template <int D>
 struct KStage {  // one step's K codes and scales of one lane
   uint32_t c[2][D / 32];
@@ -760,14 +751,16 @@ __device__ __forceinline__ float row_lse(float m, float l) {
   return l > 0.0f || l != l ? (m - P_SHIFT) * LN2 + logf(l) : -INFINITY;
 }
 
-// ---- attention of few rows over long caches -------------------------------------------------
-// The steps of all row tiles of a head, in order of sequence and tile, are one line that is cut
-// into equal parts, one workgroup each: ragged batches, single long caches and many short ones
-// load the GPU evenly, in one round of workgroups.  A part's wavefronts take its steps in turn and
-// join through LDS; a tile that a cut goes through leaves partial sums, and the workgroup that
-// finishes last joins them in order of position.
-constexpr int ROWS_WAVES = 8;
-
+// ---- pieces -------------------------------------------------------------------------------
+// A workgroup takes one piece: the steps of a row tile, or where there are more workgroups than
+// tiles an equal part of them.  `per` steps a piece are chosen on the device, from the batch's
+// actual lengths, as the fewest for which the pieces are no more than the workgroups that run at
+// once (or than the tiles), so that ragged batches, single long caches and many short ones load
+// the GPU evenly in one round.  (Cutting the steps of all tiles, end to end, into equal parts
+// loads it more evenly still, but parts that reach over two tiles pay a workgroup's start and end
+// twice, 8 us: 8 sequences of up to 4099 positions and 4 rows took 28 us, 32 of up to 8192 31 us.)
+// The pieces of a cut tile leave partial sums, and the workgroup that finishes last joins them in
+// order of position.
 // Tiles of a sequence and (an upper bound of) the steps of each; a tile that sees nothing counts
 // one step, so that its rows are written.
 __device__ __forceinline__ void seq_work(const Kv4AttnArgs& a, const Seq& s, int R, int* tiles,
@@ -783,59 +776,109 @@ __device__ __forceinline__ void seq_work(const Kv4AttnArgs& a, const Seq& s, int
   }
   *steps = max(w, 1);
 }
-// 64 sequences of the line, one a lane: where they are on it and what they hold.
-struct Chunk {
-  int b0, incl, mine, steps;  // incl: places of the chunk up to and with this sequence's
+// 64 sequences, one a lane: their tiles, the steps of a tile, and how a tile is cut.
+struct Lanes {
+  int tiles, steps, chunk, k;  // k pieces of chunk steps, the last may be shorter
   Seq s;
 };
-__device__ __forceinline__ void load_chunk(const Kv4AttnArgs& a, int R, int b0, Chunk& c) {
+__device__ __forceinline__ void load_lanes(const Kv4AttnArgs& a, int R, int b0, Lanes& c) {
   const int b = b0 + (threadIdx.x & 63);
-  int tiles = 0;
-  c.b0 = b0;
+  c.tiles = 0;
   c.steps = 1;
   c.s = Seq{0, 0, 0, 0};
   if (b < a.w.B) {
     c.s = seq_at(a.w, b);
-    seq_work(a, c.s, R, &tiles, &c.steps);
+    seq_work(a, c.s, R, &c.tiles, &c.steps);
   }
-  c.mine = tiles * c.steps;
-  c.incl = wave_incl_sum(c.mine);
 }
-// The line's length; c: its first chunk.
-__device__ __forceinline__ int line_length(const Kv4AttnArgs& a, int R, Chunk& c) {
-  int n = 0;
-  for (int b0 = (a.w.B - 1) & ~63; b0 >= 0; b0 -= 64) {
-    load_chunk(a, R, b0, c);
-    n += __builtin_amdgcn_readlane(c.incl, 63);
+__device__ __forceinline__ void cut_lanes(const Kv4AttnArgs& a, int per, Lanes& c) {
+  c.chunk = c.steps;
+  c.k = 1;
+  if (c.steps > per && c.steps > 2 * a.min_steps) {
+    const unsigned k = ((unsigned)c.steps + per - 1) / (unsigned)per;
+    // multiples of 8: a step more costs a wavefront of 8 as much as 8
+    c.chunk = (int)(((unsigned)c.steps + k - 1) / k + 7) & ~7;
+    c.k = (int)(((unsigned)c.steps + c.chunk - 1) / (unsigned)c.chunk);
   }
-  return n;
 }
-struct Spot {  // a tile on the line
-  int b, tile, steps, start;  // sequence, its tile, the tile's places and the first of them
+__device__ __forceinline__ int wave_total(int v) {
+  return __builtin_amdgcn_readlane(wave_incl_sum(v), 63);
+}
+
+struct Piece {
   Seq s;
+  int b, tile;     // sequence, and its tile
+  int s0, s1;      // steps of the tile
+  int n, index;    // pieces of the tile, and which of them this is
+  int partial;     // where its partial sums go, in units of partials
 };
-// The tile that holds place x; c: the line's first chunk (read again where it does not hold x).
-__device__ __forceinline__ Spot find_spot(const Kv4AttnArgs& a, int R, int x, Chunk& c) {
-  int before = 0;
-  while (true) {
-    const int all = __builtin_amdgcn_readlane(c.incl, 63);
-    if (x < before + all || c.b0 + 64 >= a.w.B) break;
-    before += all;
-    load_chunk(a, R, c.b0 + 64, c);
+// The x-th piece, from the last; false: there are not as many.  Uniform over the workgroup.
+__device__ __forceinline__ bool find_piece(const Kv4AttnArgs& a, int R, int x, Piece& f) {
+  Lanes c;
+  load_lanes(a, R, 0, c);
+  int per = 1 << 30;
+  if (a.part) {
+    int total = wave_total(c.tiles * c.steps), tiles = wave_total(c.tiles);
+    if (a.w.B > 64) {
+      for (int b0 = 64; b0 < a.w.B; b0 += 64) {
+        Lanes d;
+        load_lanes(a, R, b0, d);
+        total += wave_total(d.tiles * d.steps);
+      }
+      tiles = 0;
+    }
+    per = max((total + a.n_parts - 1) / a.n_parts, a.min_steps);
+    if (a.w.B <= 64) {
+      const int most = max(a.n_parts, tiles);
+      while (true) {
+        const float r = __builtin_amdgcn_rcpf((float)per);
+        if (wave_total(c.tiles * max((int)ceilf((float)c.steps * r - 1e-3f), 1)) <= most) break;
+        per += (per >> 3) + 1;
+      }
+    }
   }
-  const int i = min(__popcll(__ballot(before + c.incl <= x)), 63);
-  Spot f;
-  f.b = c.b0 + i;
-  f.steps = __builtin_amdgcn_readlane(c.steps, i);
-  const int s0 = before + __builtin_amdgcn_readlane(c.incl - c.mine, i);
-  f.tile = (x - s0) / f.steps;
-  f.start = s0 + f.tile * f.steps;
-  f.s.row0 = __builtin_amdgcn_readlane(c.s.row0, i);
-  f.s.n = __builtin_amdgcn_readlane(c.s.n, i);
-  f.s.len = __builtin_amdgcn_readlane(c.s.len, i);
-  f.s.cap = __builtin_amdgcn_readlane(c.s.cap, i);
-  if (c.b0 > 0) load_chunk(a, R, 0, c);
-  return f;
+  int pieces = 0, cuts = 0, n_pieces = 0;
+  cut_lanes(a, per, c);
+  if (a.w.B <= 64) {
+    n_pieces = wave_total(c.tiles * c.k);
+  } else {
+    for (int b0 = 0; b0 < a.w.B; b0 += 64) {
+      Lanes d;
+      load_lanes(a, R, b0, d);
+      cut_lanes(a, per, d);
+      n_pieces += wave_total(d.tiles * d.k);
+    }
+  }
+  x = n_pieces - 1 - x;  // the pieces of later tiles, which see more, first
+  if (x < 0) return false;
+  int b0 = 0;
+  while (true) {
+    const int mine = c.tiles * c.k, cut = c.k > 1 ? mine : 0;
+    const int incl = wave_incl_sum(mine), cincl = wave_incl_sum(cut);
+    const int all = __builtin_amdgcn_readlane(incl, 63);
+    if (x < pieces + all || b0 + 64 >= a.w.B) {
+      const int i = min(__popcll(__ballot(pieces + incl <= x)), 63);
+      const int at = x - (pieces + __builtin_amdgcn_readlane(incl - mine, i));
+      f.b = b0 + i;
+      f.n = __builtin_amdgcn_readlane(c.k, i);
+      f.tile = f.n > 1 ? at / f.n : at;
+      f.index = at - f.tile * f.n;
+      const int chunk = __builtin_amdgcn_readlane(c.chunk, i);
+      f.s0 = f.index * chunk;
+      f.s1 = min(f.s0 + chunk, __builtin_amdgcn_readlane(c.steps, i));
+      f.partial = cuts + __builtin_amdgcn_readlane(cincl - cut, i) + at;
+      f.s.row0 = __builtin_amdgcn_readlane(c.s.row0, i);
+      f.s.n = __builtin_amdgcn_readlane(c.s.n, i);
+      f.s.len = __builtin_amdgcn_readlane(c.s.len, i);
+      f.s.cap = __builtin_amdgcn_readlane(c.s.cap, i);
+      return true;
+    }
+    pieces += all;
+    cuts += __builtin_amdgcn_readlane(cincl, 63);
+    b0 += 64;
+    load_lanes(a, R, b0, c);
+    cut_lanes(a, per, c);
+  }
 }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t part_rsrc(const float* p) {
@@ -870,12 +913,11 @@ __device__ __forceinline__ void store_lse(const Kv4AttnArgs& a, const Tile& t, i
   if (a.lse) a.lse[(int64_t)qi * a.Hq + h] = row_lse(m, l);
 }
 
-// Joins the partials of one tile: parts first .. first + n - 1 of this head; the first left its
-// sums in its second place (the tile ends behind the part), the others in their first.  A
-// wavefront takes a row at a time; LR lanes hold a row, so it reads 64 / LR parts at once.
+// Joins the n partials of one tile, from `first` on.  A wavefront takes a row at a time; LR lanes
+// hold a row, so it reads 64 / LR partials at once.
 template <int D, int R>
-__device__ __forceinline__ void join_parts(const Kv4AttnArgs& a, const Tile& t, int part0, int first,
-                                           int n, int wave, int n_waves) {
+__device__ __forceinline__ void join_parts(const Kv4AttnArgs& a, const Tile& t, int first, int n,
+                                           int wave, int n_waves) {
   constexpr int LR = D / 4, PL = 64 / LR, SIZE = R * (D + 2);
   const int lane = threadIdx.x & 63, sub = lane / LR, d = 4 * (lane % LR);
   const __amdgpu_buffer_rsrc_t r = part_rsrc(a.part);
@@ -885,7 +927,7 @@ __device__ __forceinline__ void join_parts(const Kv4AttnArgs& a, const Tile& t, 
     for (int k0 = 0; k0 < n; k0 += 64) {
       const int k = min(k0 + lane, n - 1);
       const int here = min(n - k0, 64);
-      const int at = (2 * (part0 + first + k) + (k == 0)) * SIZE + R * D + row;
+      const int at = (first + k) * SIZE + R * D + row;
       float pm = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, at * 4, 0, 16));
       float pl = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (at + R) * 4, 0, 16));
       float f = 0.0f;
@@ -895,7 +937,7 @@ __device__ __forceinline__ void join_parts(const Kv4AttnArgs& a, const Tile& t, 
 #pragma unroll
         for (int u = 0; u < UN; ++u) {
           const int kk = k0 + min(j0 + u * PL + sub, here - 1);
-          v[u] = ld4_agent(r, (2 * (part0 + first + kk) + (kk == 0)) * SIZE + row * D + d);
+          v[u] = ld4_agent(r, (first + kk) * SIZE + row * D + d);
         }
         if (j0 == 0) {  // the chunk's weights, while the first sums are on their way
           if (lane >= here) {
@@ -933,6 +975,10 @@ __device__ __forceinline__ void join_parts(const Kv4AttnArgs& a, const Tile& t, 
   }
 }
 
+// ---- attention of few rows over long caches -------------------------------------------------
+// Wavefronts take a piece's steps in turn and join their sums through LDS.
+constexpr int ROWS_WAVES = 8;
+
 template <int D, int FMT, int NT>
 __global__ __launch_bounds__(64 * ROWS_WAVES, 2) void kv4_attn_rows_kernel(Kv4AttnArgs a) {
   constexpr int R = 16 * NT, LD = D + 4, NW = ROWS_WAVES, SIZE = R * (D + 2);
@@ -941,158 +987,132 @@ __global__ __launch_bounds__(64 * ROWS_WAVES, 2) void kv4_attn_rows_kernel(Kv4At
   __shared__ int lds_flag;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q16 = lane & 15, g = lane >> 4;
-  const int head = blockIdx.x % a.w.Hkv, part = blockIdx.x / a.w.Hkv;
-  const int part0 = head * a.n_parts;
-  const bool cut = a.part != nullptr;  // without partials a part is a whole tile
-  int x = 0, end = 0, per = 1;
-  Spot spot;
-  Chunk chunk;
-  if (cut) {
-    const int total = line_length(a, R, chunk);
-    per = max((total + a.n_parts - 1) / a.n_parts, a.min_steps);
-    per = (per + NW - 1) / NW * NW;  // a shorter part takes a wavefront as long
-    x = part * per;
-    end = min(x + per, total);
-    if (x >= end) return;
-  }
+  const int head = blockIdx.x % a.w.Hkv;
+  Piece f;
+  if (!find_piece(a, R, blockIdx.x / a.w.Hkv, f)) return;
   Tile t;
+  tile_of(a, f.s, f.b, f.tile, head, R, t);
+  const int s0 = f.s0;
+  const bool whole = f.n == 1;
   const float c = a.scale * LOG2E;
   const Offsets<D> off(a.w, lane);
-  while (true) {
-    int s0 = 0, s1;
-    bool whole = true;
-    if (cut) {
-      spot = find_spot(a, R, x, chunk);
-      tile_of(a, spot.s, spot.b, spot.tile, head, R, t);
-      s0 = x - spot.start;
-      s1 = min(end - spot.start, spot.steps);
-      whole = s0 == 0 && s1 == spot.steps;
-    } else {
-      if (!tile_at(a, part, head, R, t)) return;
-      s1 = t.n_steps;
+  if (t.s.len > t.s.cap && s0 == 0 && threadIdx.x == 0) report(a.w.status, ST_LENGTH);
+  Acc<D, NT> acc;
+  acc.clear();
+  bool all_ok = true;
+  const int last = min(f.s1, t.n_steps);
+  uint4 raw[NT][D / 32];
+  Queries<D, NT> q;
+  bool first_round = true;
+  for (int base = s0 + wave; base < last; base += 64 * NW) {
+    // pages of up to 64 of the wavefront's steps, one a lane; -1: no such page
+    int pages;
+    {
+      const int step = min(base + lane * NW, last - 1);
+      pages = a.w.table[(int64_t)t.b * a.w.max_pages + (position_of(t, step) >> a.w.page_shift)];
     }
-    if (t.s.len > t.s.cap && s0 == 0 && threadIdx.x == 0) report(a.w.status, ST_LENGTH);
-    Acc<D, NT> acc;
-    acc.clear();
-    bool all_ok = true;
-    const int last = min(s1, t.n_steps);
-    uint4 raw[NT][D / 32];
-    Queries<D, NT> q;
-    bool first_round = true;
-    for (int base = s0 + wave; base < last; base += 64 * NW) {
-      // pages of up to 64 of the wavefront's steps, one a lane; -1: no such page
-      int pages;
-      {
-        const int step = min(base + lane * NW, last - 1);
-        pages = a.w.table[(int64_t)t.b * a.w.max_pages + (position_of(t, step) >> a.w.page_shift)];
-      }
-      if (first_round) load_queries<D, NT>(a, t, q16, g, raw, q.pos);
-      if (pages < 0 || pages >= a.w.num_pages) pages = -1;
-      const int n = min((last - base + NW - 1) / NW, 64);
-      KStage<D> ks;
-      VStage<D> vs;
-      int t0 = position_of(t, base), page = __builtin_amdgcn_readlane(pages, 0);
-      Place pl = place_of<D>(a.w, head, max(page, 0), t0);
-      load_k<D>(pl, off, ks);
-      load_v<D>(pl, off, vs);
-      if (first_round) convert_queries<D, FMT, NT>(raw, q);
-      first_round = false;
+    if (first_round) load_queries<D, NT>(a, t, q16, g, raw, q.pos);
+    if (pages < 0 || pages >= a.w.num_pages) pages = -1;
+    const int n = min((last - base + NW - 1) / NW, 64);
+    KStage<D> ks;
+    VStage<D> vs;
+    int t0 = position_of(t, base), page = __builtin_amdgcn_readlane(pages, 0);
+    Place pl = place_of<D>(a.w, head, max(page, 0), t0);
+    load_k<D>(pl, off, ks);
+    load_v<D>(pl, off, vs);
+    if (first_round) convert_queries<D, FMT, NT>(raw, q);
+    first_round = false;
 #pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        if (page >= 0) {
-          f32x4_t sc[NT][2];
-          step_scores<D, FMT, NT>(ks, q, c, sc);
-          if (step_at_edge(a, t, t0)) step_mask<D, NT>(a, t, t0, g, q, sc, vs.s);
-          f16x8_t p[NT];
-          step_weights<D, FMT, NT>(sc, acc, p);
-          step_values<D, FMT, NT>(vs, p, acc);
-        } else {
-          all_ok = false;
-        }
-        if (i + 1 < n) {
-          t0 = position_of(t, base + (i + 1) * NW);
-          page = __builtin_amdgcn_readlane(pages, i + 1);
-          pl = place_of<D>(a.w, head, max(page, 0), t0);
-          load_k<D>(pl, off, ks);
-          load_v<D>(pl, off, vs);
-        }
+    for (int i = 0; i < n; ++i) {
+      if (page >= 0) {
+        f32x4_t sc[NT][2];
+        step_scores<D, FMT, NT>(ks, q, c, sc);
+        if (step_at_edge(a, t, t0)) step_mask<D, NT>(a, t, t0, g, q, sc, vs.s);
+        f16x8_t p[NT];
+        step_weights<D, FMT, NT>(sc, acc, p);
+        step_values<D, FMT, NT>(vs, p, acc);
+      } else {
+        all_ok = false;
+      }
+      if (i + 1 < n) {
+        t0 = position_of(t, base + (i + 1) * NW);
+        page = __builtin_amdgcn_readlane(pages, i + 1);
+        pl = place_of<D>(a.w, head, max(page, 0), t0);
+        load_k<D>(pl, off, ks);
+        load_v<D>(pl, off, vs);
       }
     }
-    if (!all_ok && lane == 0) report(a.w.status, ST_PAGE);
+  }
+  if (!all_ok && lane == 0) report(a.w.status, ST_PAGE);
 
-    // join the wavefronts: sums to LDS, then each wavefront adds two rows of every 16
+  // join the wavefronts: sums to LDS, then each wavefront adds two rows of every 16
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float l = acc.l[nt];
-      l += __shfl_xor(l, 16);
-      l += __shfl_xor(l, 32);
-      if (g == 0) {
-        lds_m[wave][16 * nt + q16] = acc.m[nt];
-        lds_l[wave][16 * nt + q16] = l;
-      }
+  for (int nt = 0; nt < NT; ++nt) {
+    float l = acc.l[nt];
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (g == 0) {
+      lds_m[wave][16 * nt + q16] = acc.m[nt];
+      lds_l[wave][16 * nt + q16] = l;
     }
-    const int place = 2 * (part0 + part) + (s0 == 0);
-    const __amdgpu_buffer_rsrc_t pr = part_rsrc(a.part);
+  }
+  const int partial = head * 2 * a.n_parts + f.partial;
+  const __amdgpu_buffer_rsrc_t pr = part_rsrc(a.part);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (nt > 0) __syncthreads();
-      float* dst = &lds_o[wave][q16][0];
+  for (int nt = 0; nt < NT; ++nt) {
+    if (nt > 0) __syncthreads();
+    float* dst = &lds_o[wave][q16][0];
 #pragma unroll
-      for (int e = 0; e < D / 64; ++e)
+    for (int e = 0; e < D / 64; ++e)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<float4*>(dst + 64 * e + 16 * g + 4 * i) =
-              make_float4(acc.o[nt][e][0][i], acc.o[nt][e][1][i], acc.o[nt][e][2][i],
-                          acc.o[nt][e][3][i]);
-      __syncthreads();
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<float4*>(dst + 64 * e + 16 * g + 4 * i) =
+            make_float4(acc.o[nt][e][0][i], acc.o[nt][e][1][i], acc.o[nt][e][2][i],
+                        acc.o[nt][e][3][i]);
+    __syncthreads();
 #pragma unroll
-      for (int rr = 0; rr < 16 / NW; ++rr) {
-        const int row16 = (16 / NW) * wave + rr, row = 16 * nt + row16;
-        if (row < t.n_rho) {
-          float m = lds_m[0][row];
+    for (int rr = 0; rr < 16 / NW; ++rr) {
+      const int row16 = (16 / NW) * wave + rr, row = 16 * nt + row16;
+      if (row < t.n_rho) {
+        float m = lds_m[0][row];
 #pragma unroll
-          for (int w = 1; w < NW; ++w) m = fmaxf(m, lds_m[w][row]);
-          float l = 0.0f, f[NW];
+        for (int w = 1; w < NW; ++w) m = fmaxf(m, lds_m[w][row]);
+        float l = 0.0f, f[NW];
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          f[w] = __builtin_amdgcn_exp2f(lds_m[w][row] - m);
+          l += lds_l[w][row] * f[w];
+        }
+        const int d = 4 * lane;
+        if (d < D) {
+          float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
           for (int w = 0; w < NW; ++w) {
-            f[w] = __builtin_amdgcn_exp2f(lds_m[w][row] - m);
-            l += lds_l[w][row] * f[w];
+            const float4 z = *reinterpret_cast<const float4*>(&lds_o[w][row16][d]);
+            u.x += f[w] * z.x; u.y += f[w] * z.y; u.z += f[w] * z.z; u.w += f[w] * z.w;
           }
-          const int d = 4 * lane;
-          if (d < D) {
-            float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-              const float4 z = *reinterpret_cast<const float4*>(&lds_o[w][row16][d]);
-              u.x += f[w] * z.x; u.y += f[w] * z.y; u.z += f[w] * z.z; u.w += f[w] * z.w;
-            }
-            if (whole)
-              store_out4(a, t, D, row, d, u, row_inv(l));
-            else
-              st4_agent(pr, place * SIZE + row * D + d, u);
-          }
-          if (lane == 0) {
-            if (whole) {
-              store_lse(a, t, row, m, l);
-            } else {
-              st_sc1(a.part, (size_t)place * SIZE + R * D + row, m);
-              st_sc1(a.part, (size_t)place * SIZE + R * D + R + row, l);
-            }
+          if (whole)
+            store_out4(a, t, D, row, d, u, row_inv(l));
+          else
+            st4_agent(pr, partial * SIZE + row * D + d, u);
+        }
+        if (lane == 0) {
+          if (whole) {
+            store_lse(a, t, row, m, l);
+          } else {
+            st_sc1(a.part, (size_t)partial * SIZE + R * D + row, m);
+            st_sc1(a.part, (size_t)partial * SIZE + R * D + R + row, l);
           }
         }
       }
     }
-    if (!cut) return;
-    if (!whole) {
-      const int first = spot.start / per, n = (spot.start + spot.steps - 1) / per - first + 1;
-      if (last_arriver(a.counters + part0 + first, (unsigned)n, &lds_flag)) {
-        join_parts<D, R>(a, t, part0, first, n, wave, NW);
-        if (threadIdx.x == 0) st_cnt(a.counters + part0 + first, 0u);
-      }
+  }
+  if (!whole) {
+    unsigned* counter = a.counters + head * 2 * a.n_parts + (f.partial - f.index);
+    if (last_arriver(counter, (unsigned)f.n, &lds_flag)) {
+      join_parts<D, R>(a, t, partial - f.index, f.n, wave, NW);
+      if (threadIdx.x == 0) st_cnt(counter, 0u);
     }
-    x = spot.start + s1;
-    if (x >= end) return;
-    __syncthreads();  // LDS is free again
   }
 }
 
@@ -1262,8 +1282,8 @@ __device__ __forceinline__ void tile_values(const uint4* v, P weights, f32x16_t 
 // Joins the partials of a tile of many rows: few parts, so a thread keeps 4 columns of 4 rows and
 // goes through the parts in order.
 template <int D, int R>
-__device__ __forceinline__ void join_tiles(const Kv4AttnArgs& a, const Tile& t, int part0, int first,
-                                           int n, int tid) {
+__device__ __forceinline__ void join_tiles(const Kv4AttnArgs& a, const Tile& t, int first, int n,
+                                           int tid) {
   constexpr int LR = D / 4, RS = TILE_THREADS / LR, SIZE = R * (D + 2);
   const __amdgpu_buffer_rsrc_t pr = part_rsrc(a.part);
   const int d = 4 * (tid % LR);
@@ -1277,7 +1297,7 @@ __device__ __forceinline__ void join_tiles(const Kv4AttnArgs& a, const Tile& t, 
       oo[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
     for (int k = 0; k < n; ++k) {
-      const int at = (2 * (part0 + first + k) + (k == 0)) * SIZE;
+      const int at = (first + k) * SIZE;
       float4 v[4];
       float pm[4], pl[4];
 #pragma unroll
@@ -1326,20 +1346,9 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
   // the wavefront's 32 rows, and (D = 256) its half of the positions and columns
   const int rows32 = HV == 2 ? 2 * group + ((wave & 3) >> 1) : wave, half = HV == 2 ? wave & 1 : 0;
   const int q32 = lane & 31, h = lane >> 5;
-  const int head = blockIdx.x % a.w.Hkv, part = blockIdx.x / a.w.Hkv;
-  const int part0 = head * a.n_parts;
-  const bool cut = a.part != nullptr;
-  int x = 0, end = 0, per = 1;
-  Spot spot;
-  Chunk chunk;
-  if (cut) {
-    const int total = line_length(a, R, chunk);
-    per = max((total + a.n_parts - 1) / a.n_parts, a.min_steps);
-    per = (per + 1) & ~1;
-    x = part * per;
-    end = min(x + per, total);
-    if (x >= end) return;
-  }
+  const int head = blockIdx.x % a.w.Hkv;
+  Piece f;
+  if (!find_piece(a, R, blockIdx.x / a.w.Hkv, f)) return;
   const Layout<D> L(a.w);
   const TileMap<D> map(tid);
   const TileOffsets<D> off(a.w, L, map);
@@ -1348,337 +1357,321 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
   // the sign of the scale goes to Q; 1e-30 stands for a scale of 0 (equal weights all the same)
   const float c = fmaxf(fabsf(a.scale * LOG2E), 1e-30f), move_by = MOVE / c;
   Tile t;
-  while (true) {
-    int s0 = 0, s1;
-    bool whole = true;
-    if (cut) {
-      spot = find_spot(a, R, x, chunk);
-      tile_of(a, spot.s, spot.b, spot.tile, head, R, t);
-      s0 = x - spot.start;
-      s1 = min(end - spot.start, spot.steps);
-      whole = s0 == 0 && s1 == spot.steps;
-    } else {
-      // the longest tiles first
-      if (!tile_at(a, a.n_slots - 1 - part, head, R, t)) return;
-      s1 = t.n_steps;
+  tile_of(a, f.s, f.b, f.tile, head, R, t);
+  const int s0 = f.s0;
+  const bool whole = f.n == 1;
+  if (t.s.len > t.s.cap && s0 == 0 && tid == 0) report(a.w.status, ST_LENGTH);
+  const int last = min(f.s1, t.n_steps), n_turns = last > s0 ? (last - s0 + 1) >> 1 : 0;
+  const int my0 = 32 * rows32;  // first of the wavefront's rows
+  const bool busy = my0 < t.n_rho;
+  // positions of the wavefront's first and last row
+  const int p_first = t.s.len - t.s.n;
+  const int w_lo = p_first + row_of(a, t.rho0 + min(my0, t.n_rho - 1));
+  const int w_hi = p_first + row_of(a, t.rho0 + min(my0 + 31, t.n_rho - 1));
+  const auto edge_at = [&](int t0, int lo, int hi) {
+    return t0 + KV4_STEP - 1 > lo ||
+           (a.window > 0 && t0 <= hi - a.window && t0 + KV4_STEP > a.sinks);
+  };
+  // 64 steps from list0 on, one a lane: position, offset of the codes in the cache, how far the
+  // scales are from there; and which steps some row of the workgroup, or of the wavefront,
+  // does not see whole.  A step that is not there is read somewhere and seen nowhere.
+  int list0 = s0, l_pos = NOWHERE, l_scales = 0;
+  int64_t l_codes = 0;
+  uint64_t edges = 0, my_edges = 0;
+  const auto load_list = [&](int from) {
+    list0 = from;
+    const int at = position_of(t, min(from + lane, last - 1));
+    int page = a.w.table[(int64_t)t.b * a.w.max_pages + (at >> a.w.page_shift)];
+    const bool there = page >= 0 && page < a.w.num_pages, mine = from + lane < last;
+    if (!there && mine) report(a.w.status, ST_PAGE);
+    page = there ? page : 0;
+    l_pos = there && mine ? at : NOWHERE;
+    const int in_page = at & ((1 << a.w.page_shift) - 1);
+    l_codes = page * a.w.page_bytes + (int64_t)head * a.w.head_bytes + in_page * (D / 2);
+    l_scales = ((in_page << L.n_shift) << 1) - in_page * (D / 2);
+    edges = __ballot(edge_at(l_pos, t.p_lo, t.p_hi));
+    my_edges = __ballot(edge_at(l_pos, w_lo, w_hi));
+  };
+  // where the thread reads its codes of a turn
+  const uint8_t* codes = a.w.cache;
+  uint32_t scales = 0;
+  const auto go_to = [&](int turn) {
+    const int i = s0 + 2 * turn + group - list0;
+    codes = a.w.cache + (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(l_codes >> 32), i) << 32) |
+                                  (uint32_t)__builtin_amdgcn_readlane((int)l_codes, i));
+    scales = (uint32_t)__builtin_amdgcn_readlane(l_scales, i);
+  };
+  TileStage<D> st;
+  uint32_t vs_now[NE][4];  // V scales of the turn whose V is decoded next
+  const auto decode_k = [&](int turn) {  // K of a turn, and its V scales to vs_now
+    const _Float16 s1 = (_Float16)bf16_to_f32(st.ks);
+    const f16x2_t s = {s1, s1}, s24 = s * (f16x2_t){(_Float16)-24.0f, (_Float16)-24.0f};
+    const f16x2_t s4[4] = {s, s, s, s}, z4[4] = {s24, s24, s24, s24};
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      lds_k[turn & 1][map.kd + i][map.tok] =
+          __builtin_bit_cast(uint4, decode_f16<FMT>(st.k[i], s4, z4));
+#pragma unroll
+    for (int e = 0; e < NE; ++e) {
+      vs_now[e][0] = st.vs[e].x; vs_now[e][1] = st.vs[e].y;
+      vs_now[e][2] = st.vs[e].z; vs_now[e][3] = st.vs[e].w;
     }
-    if (t.s.len > t.s.cap && s0 == 0 && tid == 0) report(a.w.status, ST_LENGTH);
-    const int last = min(s1, t.n_steps), n_turns = last > s0 ? (last - s0 + 1) >> 1 : 0;
-    const int my0 = 32 * rows32;  // first of the wavefront's rows
-    const bool busy = my0 < t.n_rho;
-    // positions of the wavefront's first and last row
-    const int p_first = t.s.len - t.s.n;
-    const int w_lo = p_first + row_of(a, t.rho0 + min(my0, t.n_rho - 1));
-    const int w_hi = p_first + row_of(a, t.rho0 + min(my0 + 31, t.n_rho - 1));
-    const auto edge_at = [&](int t0, int lo, int hi) {
-      return t0 + KV4_STEP - 1 > lo ||
-             (a.window > 0 && t0 <= hi - a.window && t0 + KV4_STEP > a.sinks);
-    };
-    // 64 steps from list0 on, one a lane: position, offset of the codes in the cache, how far the
-    // scales are from there; and which steps some row of the workgroup, or of the wavefront,
-    // does not see whole.  A step that is not there is read somewhere and seen nowhere.
-    int list0 = s0, l_pos = NOWHERE, l_scales = 0;
-    int64_t l_codes = 0;
-    uint64_t edges = 0, my_edges = 0;
-    const auto load_list = [&](int from) {
-      list0 = from;
-      const int at = position_of(t, min(from + lane, last - 1));
-      int page = a.w.table[(int64_t)t.b * a.w.max_pages + (at >> a.w.page_shift)];
-      const bool there = page >= 0 && page < a.w.num_pages, mine = from + lane < last;
-      if (!there && mine) report(a.w.status, ST_PAGE);
-      page = there ? page : 0;
-      l_pos = there && mine ? at : NOWHERE;
-      const int in_page = at & ((1 << a.w.page_shift) - 1);
-      l_codes = page * a.w.page_bytes + (int64_t)head * a.w.head_bytes + in_page * (D / 2);
-      l_scales = ((in_page << L.n_shift) << 1) - in_page * (D / 2);
-      edges = __ballot(edge_at(l_pos, t.p_lo, t.p_hi));
-      my_edges = __ballot(edge_at(l_pos, w_lo, w_hi));
-    };
-    // where the thread reads its codes of a turn
-    const uint8_t* codes = a.w.cache;
-    uint32_t scales = 0;
-    const auto go_to = [&](int turn) {
-      const int i = s0 + 2 * turn + group - list0;
-      codes = a.w.cache + (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(l_codes >> 32), i) << 32) |
-                                    (uint32_t)__builtin_amdgcn_readlane((int)l_codes, i));
-      scales = (uint32_t)__builtin_amdgcn_readlane(l_scales, i);
-    };
-    TileStage<D> st;
-    uint32_t vs_now[NE][4];  // V scales of the turn whose V is decoded next
-    const auto decode_k = [&](int turn) {  // K of a turn, and its V scales to vs_now
-      const _Float16 s1 = (_Float16)bf16_to_f32(st.ks);
-      const f16x2_t s = {s1, s1}, s24 = s * (f16x2_t){(_Float16)-24.0f, (_Float16)-24.0f};
-      const f16x2_t s4[4] = {s, s, s, s}, z4[4] = {s24, s24, s24, s24};
+    if ((edges >> (s0 + 2 * turn + group - list0)) & 1) {
+      // scales that fp16 cannot take: cleared, and the rows that see them are told.  (In a step
+      // that all rows see whole they do their damage by themselves.)
+      uint32_t over[4], any_over = 0, any = 0;
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        lds_k[turn & 1][map.kd + i][map.tok] =
-            __builtin_bit_cast(uint4, decode_f16<FMT>(st.k[i], s4, z4));
+      for (int i = 0; i < 4; ++i) {
+        over[i] = above_limit<FMT>(vs_now[0][i]);
 #pragma unroll
-      for (int e = 0; e < NE; ++e) {
-        vs_now[e][0] = st.vs[e].x; vs_now[e][1] = st.vs[e].y;
-        vs_now[e][2] = st.vs[e].z; vs_now[e][3] = st.vs[e].w;
+        for (int e = 1; e < NE; ++e) over[i] |= above_limit<FMT>(vs_now[e][i]);
+        any_over |= over[i];
       }
-      if ((edges >> (s0 + 2 * turn + group - list0)) & 1) {
-        // scales that fp16 cannot take: cleared, and the rows that see them are told.  (In a step
-        // that all rows see whole they do their damage by themselves.)
-        uint32_t over[4], any_over = 0, any = 0;
+      if (__ballot(any_over != 0)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          over[i] = above_limit<FMT>(vs_now[0][i]);
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t h16 = (i & 1) ? 0xFFFF0000u : 0x0000FFFFu;
+          const bool bad = (over[i / 2] & h16) != 0;
+          any |= __ballot(bad) ? 1u << i : 0u;
 #pragma unroll
-          for (int e = 1; e < NE; ++e) over[i] |= above_limit<FMT>(vs_now[e][i]);
-          any_over |= over[i];
+          for (int e = 0; e < NE; ++e) vs_now[e][i / 2] &= bad ? ~h16 : ~0u;
         }
-        if (__ballot(any_over != 0)) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t h16 = (i & 1) ? 0xFFFF0000u : 0x0000FFFFu;
-            const bool bad = (over[i / 2] & h16) != 0;
-            any |= __ballot(bad) ? 1u << i : 0u;
-#pragma unroll
-            for (int e = 0; e < NE; ++e) vs_now[e][i / 2] &= bad ? ~h16 : ~0u;
-          }
-        }
-        if (lane == 0) lds_bad[turn & 3][wave] = any;
       }
-    };
-    const auto decode_v = [&](int turn) {
+      if (lane == 0) lds_bad[turn & 3][wave] = any;
+    }
+  };
+  const auto decode_v = [&](int turn) {
 #pragma unroll
-      for (int e = 0; e < NE; ++e) {
-        f16x2_t vs[4], vs24[4];
+    for (int e = 0; e < NE; ++e) {
+      f16x2_t vs[4], vs24[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int i0 = value_at<FMT>(2 * i), i1 = value_at<FMT>(2 * i + 1);
-          vs[i] = f16x2_t{
-              (_Float16)((i0 & 1) ? bf16_hi(vs_now[e][i0 / 2]) : bf16_lo(vs_now[e][i0 / 2])),
-              (_Float16)((i1 & 1) ? bf16_hi(vs_now[e][i1 / 2]) : bf16_lo(vs_now[e][i1 / 2]))};
-          vs24[i] = vs[i] * (f16x2_t){(_Float16)-24.0f, (_Float16)-24.0f};
-        }
-#pragma unroll
-        for (int i = 2 * e; i < N && i < 2 * e + 2; ++i)
-          lds_v[turn & 1][map.blk][map.vd + v_step(i)] =
-              __builtin_bit_cast(uint4, decode_f16<FMT>(st.v[i], vs, vs24));
+      for (int i = 0; i < 4; ++i) {
+        const int i0 = value_at<FMT>(2 * i), i1 = value_at<FMT>(2 * i + 1);
+        vs[i] = f16x2_t{
+            (_Float16)((i0 & 1) ? bf16_hi(vs_now[e][i0 / 2]) : bf16_lo(vs_now[e][i0 / 2])),
+            (_Float16)((i1 & 1) ? bf16_hi(vs_now[e][i1 / 2]) : bf16_lo(vs_now[e][i1 / 2]))};
+        vs24[i] = vs[i] * (f16x2_t){(_Float16)-24.0f, (_Float16)-24.0f};
       }
-    };
+#pragma unroll
+      for (int i = 2 * e; i < N && i < 2 * e + 2; ++i)
+        lds_v[turn & 1][map.blk][map.vd + v_step(i)] =
+            __builtin_bit_cast(uint4, decode_f16<FMT>(st.v[i], vs, vs24));
+    }
+  };
 
-    if (n_turns > 0) {
-      load_list(s0);
-      go_to(0);
-      tile_load_k<D>(codes, scales, off, st);
-    }
-    f16x8_t q[D / 16];
-    int pos;
-    {
-      const int rho = t.rho0 + my0 + q32;
-      const bool on = my0 + q32 < t.n_rho;
-      const int i = row_of(a, rho), hh = t.head * a.r + rho - i * a.r;
-      pos = on ? p_first + i : -1;
-      const uint16_t* p = a.q + (int64_t)(t.s.row0 + i) * a.q_stride + (int64_t)hh * D + 8 * h;
-      const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
+  if (n_turns > 0) {
+    load_list(s0);
+    go_to(0);
+    tile_load_k<D>(codes, scales, off, st);
+  }
+  f16x8_t q[D / 16];
+  int pos;
+  {
+    const int rho = t.rho0 + my0 + q32;
+    const bool on = my0 + q32 < t.n_rho;
+    const int i = row_of(a, rho), hh = t.head * a.r + rho - i * a.r;
+    pos = on ? p_first + i : -1;
+    const uint16_t* p = a.q + (int64_t)(t.s.row0 + i) * a.q_stride + (int64_t)hh * D + 8 * h;
+    const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (on) u = *reinterpret_cast<const uint4*>(p + 16 * j);
-        const uint32_t uw[4] = {u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip};
+    for (int j = 0; j < D / 16; ++j) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (on) u = *reinterpret_cast<const uint4*>(p + 16 * j);
+      const uint32_t uw[4] = {u.x ^ flip, u.y ^ flip, u.z ^ flip, u.w ^ flip};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int d = value_at<FMT>(e);
-          q[j][e] = (_Float16)((d & 1) ? bf16_hi(uw[d / 2]) : bf16_lo(uw[d / 2]));
-        }
+      for (int e = 0; e < 8; ++e) {
+        const int d = value_at<FMT>(e);
+        q[j][e] = (_Float16)((d & 1) ? bf16_hi(uw[d / 2]) : bf16_lo(uw[d / 2]));
       }
     }
-    f32x16_t o[NJ], sc[NU];
+  }
+  f32x16_t o[NJ], sc[NU];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j)
+  for (int j = 0; j < NJ; ++j)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[j][i] = 0.0f;
-    float m = -FLT_MAX, l = 0.0f;  // m: of the scores before scaling
-    // hides what the rows do not see of a turn's scores; the lane's largest score
-    const auto mask_scores = [&](int turn) {
-      float mx;
-                const int i0 = s0 + 2 * turn + (HV == 2 ? half : 0) - list0;
-                constexpr uint64_t UM = (1u << NU) - 1;
-                if ((edges >> i0) & UM) {
-      #pragma unroll
-                  for (int u = 0; u < NU; ++u) {
-                    uint32_t bad = 0;
-                    if ((edges >> (i0 + u)) & 1)
-      #pragma unroll
-                      for (int b = 0; b < 4; ++b)
-                        bad |= lds_bad[turn & 3][4 * (HV == 2 ? half : u) + b] << (8 * b);
-                    if (!((my_edges >> (i0 + u)) & 1) && bad == 0) continue;
-                    const int t0 = __builtin_amdgcn_readlane(l_pos, i0 + u);
-                    // against the constant offset of a register's position
-                    const int to = pos - t0 - 8 * h, from = a.window > 0 ? to - a.window : -1000;
-                    const int first = a.sinks - t0 - 8 * h;
-      #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                      const int at = 16 * (i >> 3) + (i & 7);
-                      const bool seen = at <= to && (at > from || at < first);
-                      sc[u][i] = seen ? sc[u][i] : -INFINITY;
-                    }
-                    if (bad) {
-                      const uint32_t mine = bad >> (8 * h);
-      #pragma unroll
-                      for (int i = 0; i < 16; ++i)
-                        if ((mine >> (16 * (i >> 3) + (i & 7))) & 1 && sc[u][i] != -INFINITY)
-                          sc[u][i] = NAN;
-                    }
+    for (int i = 0; i < 16; ++i) o[j][i] = 0.0f;
+  float m = -FLT_MAX, l = 0.0f;  // m: of the scores before scaling
+  // hides what the rows do not see of a turn's scores; the lane's largest score
+  const auto mask_scores = [&](int turn) {
+    float mx;
+              const int i0 = s0 + 2 * turn + (HV == 2 ? half : 0) - list0;
+              constexpr uint64_t UM = (1u << NU) - 1;
+              if ((edges >> i0) & UM) {
+    #pragma unroll
+                for (int u = 0; u < NU; ++u) {
+                  uint32_t bad = 0;
+                  if ((edges >> (i0 + u)) & 1)
+    #pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                      bad |= lds_bad[turn & 3][4 * (HV == 2 ? half : u) + b] << (8 * b);
+                  if (!((my_edges >> (i0 + u)) & 1) && bad == 0) continue;
+                  const int t0 = __builtin_amdgcn_readlane(l_pos, i0 + u);
+                  // against the constant offset of a register's position
+                  const int to = pos - t0 - 8 * h, from = a.window > 0 ? to - a.window : -1000;
+                  const int first = a.sinks - t0 - 8 * h;
+    #pragma unroll
+                  for (int i = 0; i < 16; ++i) {
+                    const int at = 16 * (i >> 3) + (i & 7);
+                    const bool seen = at <= to && (at > from || at < first);
+                    sc[u][i] = seen ? sc[u][i] : -INFINITY;
+                  }
+                  if (bad) {
+                    const uint32_t mine = bad >> (8 * h);
+    #pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                      if ((mine >> (16 * (i >> 3) + (i & 7))) & 1 && sc[u][i] != -INFINITY)
+                        sc[u][i] = NAN;
                   }
                 }
-                mx = fmaxf(sc[0][0], sc[NU - 1][0]);
-      #pragma unroll
-                for (int i = 1; i < 16; ++i) mx = fmaxf(fmaxf(mx, sc[0][i]), sc[NU - 1][i]);
-      return mx;
-    };
-    const auto move_reference = [&](float mx) {  // mx: of the row
-      if (__ballot(mx > m + move_by)) {
-        if constexpr (HV == 1) mx = fmaxf(mx, __shfl_xor(mx, 32));
-        mx = fmaxf(mx, m);
-        const float f = __builtin_amdgcn_exp2f((m - mx) * c);
-        m = mx;
-        l *= f;
+              }
+              mx = fmaxf(sc[0][0], sc[NU - 1][0]);
+    #pragma unroll
+              for (int i = 1; i < 16; ++i) mx = fmaxf(fmaxf(mx, sc[0][i]), sc[NU - 1][i]);
+    return mx;
+  };
+  const auto move_reference = [&](float mx) {  // mx: of the row
+    if (__ballot(mx > m + move_by)) {
+      if constexpr (HV == 1) mx = fmaxf(mx, __shfl_xor(mx, 32));
+      mx = fmaxf(mx, m);
+      const float f = __builtin_amdgcn_exp2f((m - mx) * c);
+      m = mx;
+      l *= f;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) o[j] *= f;
-      }
-      return P_SHIFT - fmaxf(m * c, -FLT_MAX);
-    };
-    // the weights of the b-th 16 positions of the wavefront
-    const auto weights = [&](int b, float ref) {
-      float e[8];
-      f16x8_t w;
+      for (int j = 0; j < NJ; ++j) o[j] *= f;
+    }
+    return P_SHIFT - fmaxf(m * c, -FLT_MAX);
+  };
+  // the weights of the b-th 16 positions of the wavefront
+  const auto weights = [&](int b, float ref) {
+    float e[8];
+    f16x8_t w;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        e[i] = __builtin_amdgcn_exp2f(fmaf(sc[b >> 1][8 * (b & 1) + i], c, ref));
-      l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+    for (int i = 0; i < 8; ++i)
+      e[i] = __builtin_amdgcn_exp2f(fmaf(sc[b >> 1][8 * (b & 1) + i], c, ref));
+    l += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = (_Float16)e[value_at<FMT>(i)];
-      return w;
-    };
-    if constexpr (HV == 1) {
-      if (n_turns > 0) {
-        const auto decode_next = [&](int k) {
-          if (k >= n_turns) return;
-          decode_k(k);
-          decode_v(k);
-          if (k + 1 >= n_turns) return;
-          // (the list has the scores of turn k - 1 and K of turn k + 1)
-          if (s0 + 2 * k + 4 > list0 + 64) load_list(s0 + 2 * (k - 1));
-          go_to(k + 1);
-          tile_load_k<D>(codes, scales, off, st);
-          tile_load_v<D>(codes, off, st);
-        };
-        tile_load_v<D>(codes, off, st);
-        decode_next(0);
-        __syncthreads();
-#pragma unroll 1
-        for (int turn = 0; turn < n_turns; ++turn) {
-          if (group == 1) decode_next(turn + 1);
-          tile_scores<D, NU>(&lds_k[turn & 1][h][k_tok], q, sc);
-          const float ref = move_reference(mask_scores(turn));
-          tile_values<D, NJ>(&lds_v[turn & 1][h][q32], [&](int b) { return weights(b, ref); }, o);
-          if (group == 0) decode_next(turn + 1);
-          __syncthreads();
-        }
-      }
-    } else if (n_turns > 0) {
-      // K of turn k and V of the turn before from their codes to LDS, and the next codes' loads
-      const auto decode_turn = [&](int k) {
-        if (k > n_turns) return;
-        decode_v(k - 1);
+    for (int i = 0; i < 8; ++i) w[i] = (_Float16)e[value_at<FMT>(i)];
+    return w;
+  };
+  if constexpr (HV == 1) {
+    if (n_turns > 0) {
+      const auto decode_next = [&](int k) {
         if (k >= n_turns) return;
         decode_k(k);
-        tile_load_v<D>(codes, off, st);
+        decode_v(k);
         if (k + 1 >= n_turns) return;
-        // (the list has the scores of turn k - 2 at the earliest, K of turn k + 1 at the latest)
-        if (s0 + 2 * k + 4 > list0 + 64) load_list(s0 + 2 * max(k - 2, 0));
+        // (the list has the scores of turn k - 1 and K of turn k + 1)
+        if (s0 + 2 * k + 4 > list0 + 64) load_list(s0 + 2 * (k - 1));
         go_to(k + 1);
         tile_load_k<D>(codes, scales, off, st);
+        tile_load_v<D>(codes, off, st);
       };
-      const auto values = [&](int turn) {
-        tile_values<D, NJ>(&lds_v[turn & 1][h][32 * NJ * half + q32], [&](int b) {
-          return __builtin_bit_cast(f16x8_t, lds_p[rows32][b][lane]);
-        }, o);
-      };
-      decode_k(0);
       tile_load_v<D>(codes, off, st);
-      if (n_turns > 1) {
-        go_to(1);
-        tile_load_k<D>(codes, scales, off, st);
-      }
+      decode_next(0);
       __syncthreads();
-      if (group == 1) {  // half a turn behind group 0
-        decode_turn(1);
-        __syncthreads();
-      }
 #pragma unroll 1
       for (int turn = 0; turn < n_turns; ++turn) {
-        // phase M
-        __builtin_amdgcn_s_setprio(1);
-        if (turn > 0) values(turn - 1);
-        tile_scores<D, NU>(&lds_k[turn & 1][h][32 * half + k_tok], q, sc);
-        __builtin_amdgcn_s_setprio(0);
-        float mx = mask_scores(turn);
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
-        if (h == 0) lds_m[rows32][half][q32] = mx;
-        __syncthreads();
-        // phase A
-        mx = fmaxf(mx, lds_m[rows32][half ^ 1][q32]);
-        const float ref = move_reference(mx);
-#pragma unroll
-        for (int b = 0; b < 2 * NU; ++b)
-          lds_p[rows32][2 * half + b][lane] = __builtin_bit_cast(uint4, weights(b, ref));
-        decode_turn(turn + 1 + group);
+        if (group == 1) decode_next(turn + 1);
+        tile_scores<D, NU>(&lds_k[turn & 1][h][k_tok], q, sc);
+        const float ref = move_reference(mask_scores(turn));
+        tile_values<D, NJ>(&lds_v[turn & 1][h][q32], [&](int b) { return weights(b, ref); }, o);
+        if (group == 0) decode_next(turn + 1);
         __syncthreads();
       }
-      values(n_turns - 1);
-      if (group == 0) __syncthreads();
     }
-
-    l += __shfl_xor(l, 32);
-    if constexpr (HV == 2) {
-      if (h == 0) lds_m[rows32][half][q32] = l;
-      __syncthreads();
-      l = lds_m[rows32][0][q32] + lds_m[rows32][1][q32];
+  } else if (n_turns > 0) {
+    // K of turn k and V of the turn before from their codes to LDS, and the next codes' loads
+    const auto decode_turn = [&](int k) {
+      if (k > n_turns) return;
+      decode_v(k - 1);
+      if (k >= n_turns) return;
+      decode_k(k);
+      tile_load_v<D>(codes, off, st);
+      if (k + 1 >= n_turns) return;
+      // (the list has the scores of turn k - 2 at the earliest, K of turn k + 1 at the latest)
+      if (s0 + 2 * k + 4 > list0 + 64) load_list(s0 + 2 * max(k - 2, 0));
+      go_to(k + 1);
+      tile_load_k<D>(codes, scales, off, st);
+    };
+    const auto values = [&](int turn) {
+      tile_values<D, NJ>(&lds_v[turn & 1][h][32 * NJ * half + q32], [&](int b) {
+        return __builtin_bit_cast(f16x8_t, lds_p[rows32][b][lane]);
+      }, o);
+    };
+    decode_k(0);
+    tile_load_v<D>(codes, off, st);
+    if (n_turns > 1) {
+      go_to(1);
+      tile_load_k<D>(codes, scales, off, st);
     }
-    const float m2 = l != 0.0f ? m * c : -FLT_MAX;  // in powers of 2, as the other kernel's
-    const int row = my0 + q32, place = 2 * (part0 + part) + (s0 == 0);
-    const int d0 = 32 * NJ * half + 4 * h;
-    if (row < t.n_rho) {
-      if (whole) {
-        const float inv = row_inv(l);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            store_out4(a, t, D, row, d0 + 32 * j + 2 * i,
-                       make_float4(o[j][i], o[j][i + 1], o[j][i + 2], o[j][i + 3]), inv);
-        if (d0 == 0) store_lse(a, t, row, m2, l);
-      } else {
-        const __amdgpu_buffer_rsrc_t pr = part_rsrc(a.part);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-#pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            st4_agent(pr, place * SIZE + row * D + d0 + 32 * j + 2 * i,
-                      make_float4(o[j][i], o[j][i + 1], o[j][i + 2], o[j][i + 3]));
-        if (d0 == 0) {
-          st_sc1(a.part, (size_t)place * SIZE + R * D + row, m2);
-          st_sc1(a.part, (size_t)place * SIZE + R * D + R + row, l);
-        }
-      }
-    }
-    if (!cut) return;
-    if (!whole) {
-      const int first = spot.start / per, n = (spot.start + spot.steps - 1) / per - first + 1;
-      if (last_arriver(a.counters + part0 + first, (unsigned)n, &lds_flag)) {
-        join_tiles<D, R>(a, t, part0, first, n, tid);
-        if (tid == 0) st_cnt(a.counters + part0 + first, 0u);
-      }
-    }
-    x = spot.start + s1;
-    if (x >= end) return;
     __syncthreads();
+    if (group == 1) {  // half a turn behind group 0
+      decode_turn(1);
+      __syncthreads();
+    }
+#pragma unroll 1
+    for (int turn = 0; turn < n_turns; ++turn) {
+      // phase M
+      __builtin_amdgcn_s_setprio(1);
+      if (turn > 0) values(turn - 1);
+      tile_scores<D, NU>(&lds_k[turn & 1][h][32 * half + k_tok], q, sc);
+      __builtin_amdgcn_s_setprio(0);
+      float mx = mask_scores(turn);
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      if (h == 0) lds_m[rows32][half][q32] = mx;
+      __syncthreads();
+      // phase A
+      mx = fmaxf(mx, lds_m[rows32][half ^ 1][q32]);
+      const float ref = move_reference(mx);
+#pragma unroll
+      for (int b = 0; b < 2 * NU; ++b)
+        lds_p[rows32][2 * half + b][lane] = __builtin_bit_cast(uint4, weights(b, ref));
+      decode_turn(turn + 1 + group);
+      __syncthreads();
+    }
+    values(n_turns - 1);
+    if (group == 0) __syncthreads();
+  }
+
+  l += __shfl_xor(l, 32);
+  if constexpr (HV == 2) {
+    if (h == 0) lds_m[rows32][half][q32] = l;
+    __syncthreads();
+    l = lds_m[rows32][0][q32] + lds_m[rows32][1][q32];
+  }
+  const float m2 = l != 0.0f ? m * c : -FLT_MAX;  // in powers of 2, as the other kernel's
+  const int row = my0 + q32, partial = head * 2 * a.n_parts + f.partial;
+  const int d0 = 32 * NJ * half + 4 * h;
+  if (row < t.n_rho) {
+    if (whole) {
+      const float inv = row_inv(l);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          store_out4(a, t, D, row, d0 + 32 * j + 2 * i,
+                     make_float4(o[j][i], o[j][i + 1], o[j][i + 2], o[j][i + 3]), inv);
+      if (d0 == 0) store_lse(a, t, row, m2, l);
+    } else {
+      const __amdgpu_buffer_rsrc_t pr = part_rsrc(a.part);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          st4_agent(pr, partial * SIZE + row * D + d0 + 32 * j + 2 * i,
+                    make_float4(o[j][i], o[j][i + 1], o[j][i + 2], o[j][i + 3]));
+      if (d0 == 0) {
+        st_sc1(a.part, (size_t)partial * SIZE + R * D + row, m2);
+        st_sc1(a.part, (size_t)partial * SIZE + R * D + R + row, l);
+      }
+    }
+  }
+  if (!whole) {
+    unsigned* counter = a.counters + head * 2 * a.n_parts + (f.partial - f.index);
+    if (last_arriver(counter, (unsigned)f.n, &lds_flag)) {
+      join_tiles<D, R>(a, t, partial - f.index, f.n, tid);
+      if (tid == 0) st_cnt(counter, 0u);
+    }
   }
 }
 
@@ -1695,7 +1688,7 @@ hipError_t launch_rows(const Kv4RowsArgs& a, hipStream_t st) {
 
 template <int D, int FMT>
 hipError_t launch_attn(const Kv4AttnArgs& a, hipStream_t st) {
-  const unsigned grid = (unsigned)a.w.Hkv * (a.part ? a.n_parts : a.n_slots);
+  const unsigned grid = (unsigned)a.w.Hkv * a.n_groups;
   if (a.nt == kv4_tile_nt(D)) {
     kv4_attn_tiles_kernel<D, FMT><<<grid, TILE_THREADS, 0, st>>>(a);
     return hipGetLastError();
