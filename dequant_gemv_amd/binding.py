@@ -33,6 +33,8 @@ FMT_FEXC = 4
 PATH_FORCE_GEMV = 0x100
 PATH_FORCE_MFMA = 0x200
 PATH_NO_FUSED = 0x400
+KV4_FORCE_FEW = 0x1000
+KV4_FORCE_MANY = 0x2000
 
 # (name, restype, argtypes) for every symbol the header declares
 _P = ctypes.c_void_p

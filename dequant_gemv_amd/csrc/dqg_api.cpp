@@ -307,8 +307,8 @@ constexpr int kKv4MaxHeads = 1024;
 constexpr int kKv4Resident = 256;
 constexpr int kKv4MinSteps = 8;       // steps of a piece, at least: one for each wavefront
 constexpr int kKv4MinTileSteps = 16;  // the same of the kernel for many rows: 8 turns
-// rows (query rows times the query heads of a kv head) of a sequence from which on it goes to the
-// kernel for many rows
+// rows (query rows times the query heads of a kv head) of a sequence up to which the kernel for few
+// rows takes it without weighing the two
 constexpr int kKv4FewRows = 32;
 
 inline bool kv4_heads_ok(int Hkv, int D) {
@@ -327,6 +327,20 @@ int kv4_parts(int Hkv) { return std::max(kKv4Resident / Hkv, 1); }
 size_t kv4_counter_bytes(int Hkv) { return up256(sizeof(unsigned) * 2 * Hkv * kv4_parts(Hkv)); }
 long long kv4_steps(long long positions) {
   return (positions + dqg::KV4_STEP - 1) / dqg::KV4_STEP;
+}
+// Microseconds that a kernel takes for `tiles` row tiles of `steps` steps: `round` for a workgroup
+// besides its steps, `step` for `width` steps that its wavefronts do at a time, in as many rounds
+// as the workgroups need; cut tiles trade partial sums.  Measured on the two kernels over 70 shapes
+// (1 to 47 sequences, 5 to 4079 rows, 7 to 21833 positions, windows of 2 to 5853): the choice by
+// the smaller estimate came within 4 % of the better kernel on average, where the kernel for few
+// rows throughout took 14 % longer, and the one for many rows 36 %.
+double kv4_estimate(double tiles, double steps, int min_steps, double round, double step, int width,
+                    double trade) {
+  const double n = std::max(tiles, std::min((double)kKv4Resident, tiles * steps / min_steps));
+  const double per = std::ceil(tiles * steps / n / width);
+  const double pieces = n / tiles;
+  return std::max(1.0, n / kKv4Resident) * (round + step * per) +
+         (pieces > 1.0 ? trade * (1.0 + 0.05 * pieces) : 0.0);
 }
 bool kv4_attn_sizes_ok(int T, int B, int Hq, int Hkv, int D) {
   return T >= 1 && T <= kKv4MaxT && B >= 1 && B <= kKv4MaxB && kv4_heads_ok(Hkv, D) && Hq >= 1 &&
@@ -718,9 +732,12 @@ int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32
                   int group, int format, float scale, int window, int sinks, int max_rows,
                   int max_kv_len, uint16_t* out, int64_t out_stride, float* lse, int* status,
                   void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  const int force = format & (DQG_KV4_FORCE_FEW | DQG_KV4_FORCE_MANY);
+  format &= ~force;
   int rc = check_kv4_where(T, B, cu_rows, kv_lens, block_table, max_pages, cache, num_pages, Hkv,
                            D, page_size, group, format, status);
   if (rc != DQG_OK) return rc;
+  if (force == (DQG_KV4_FORCE_FEW | DQG_KV4_FORCE_MANY)) return DQG_ERR_INVALID_ARG;
   if (Hq < 1 || Hq % Hkv || !std::isfinite(scale) || window < 0 || sinks < 0 || max_rows < 0 ||
       max_kv_len < 0)
     return DQG_ERR_INVALID_ARG;
@@ -734,9 +751,6 @@ int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32
   const int most = max_kv_len ? std::min(max_kv_len, cap) : cap;
   if (workspace && workspace_bytes < kv4_attention_workspace_bytes(T, B, Hq, Hkv, D, most))
     return DQG_ERR_WORKSPACE;
-  long long steps = kv4_steps(most);
-  if (window > 0)  // a tile of up to 256 rows sees `window` positions a row and the first ones
-    steps = std::min(steps, kv4_steps((long long)window + 256) + 1 + kv4_steps(sinks));
   dqg::Kv4AttnArgs a{};
   a.w = kv4_where(T, B, cu_rows, kv_lens, block_table, max_pages, cache, num_pages, Hkv, D,
                   page_size, group, status);
@@ -745,38 +759,55 @@ int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32
   a.r_shift = a.r > 1 ? 32 - __builtin_clz((unsigned)(a.r - 1)) : 0;
   a.r_mul = (uint32_t)(((1ull << 32) * ((1ull << a.r_shift) - a.r)) / a.r + 1);
   const int rows = std::max(std::min(max_rows ? max_rows : T, T), (T + B - 1) / B);
-  const int few = kKv4FewRows / a.r;  // rows of a sequence that are few
-  const auto launch = [&](int nt, int over, int to, int min_steps) -> int {
-    const int R = 16 * nt;
-    a.nt = nt;
+  // tiles of R rows of one head, and their steps, at most
+  const auto tiles_of = [&](int R) {
+    return std::min((long long)T * a.r / R + B, (long long)B * (((long long)rows * a.r + R - 1) / R));
+  };
+  const auto steps_of = [&](int R) {
+    const long long all = kv4_steps(most);
+    if (window == 0) return all;
+    return std::min(all, kv4_steps((long long)window + R / a.r + 1) + 1 + kv4_steps(sinks));
+  };
+  // one 16-row tile holds a token's heads; two share the decoded keys and values
+  const int nt = (long long)rows * a.r <= 16 || D > 128 ? 1 : 2, nt_many = dqg::kv4_tile_nt(D);
+  const auto launch = [&](int tiles16, int over, int to) -> int {
+    const int R = 16 * tiles16, min_steps = tiles16 == nt_many ? kKv4MinTileSteps : kKv4MinSteps;
+    a.nt = tiles16;
     a.rows_over = over;
     a.rows_to = to;
     a.min_steps = min_steps;
-    // sum of ceil(n r / R) over the sequences; pieces are at most tiles + parts
-    const long long most = (long long)T * a.r / R + B;
-    const long long tiles = std::min(most, (long long)B * (((long long)rows * a.r + R - 1) / R));
     // (hints may be wrong: any n_parts gives the right result)
-    a.n_parts = (int)std::max(1LL, std::min<long long>(kv4_parts(Hkv), (tiles * steps + min_steps - 1) / min_steps));
+    a.n_parts = (int)std::max(1LL, std::min<long long>(kv4_parts(Hkv), (tiles_of(R) * steps_of(R) + min_steps - 1) /
+                                                                           min_steps));
+    // sum of ceil(n r / R) over the sequences; pieces are at most tiles + parts
+    const long long tiles = (long long)T * a.r / R + B;
     // places in a batch's steps are 32-bit
-    const bool cut = workspace && most * (cap / dqg::KV4_STEP) < (1LL << 30);
+    const bool cut = workspace && tiles * (cap / dqg::KV4_STEP) < (1LL << 30);
     a.counters = cut ? static_cast<unsigned*>(workspace) : nullptr;
     a.part = cut ? reinterpret_cast<float*>(static_cast<char*>(workspace) + kv4_counter_bytes(Hkv))
                  : nullptr;
-    a.n_groups = (int)(most + (cut ? a.n_parts : 0));
+    a.n_groups = (int)(tiles + (cut ? a.n_parts : 0));
     if ((long long)a.n_groups * Hkv >= (1LL << 31)) return DQG_ERR_UNSUPPORTED;
     return dqg::launch_kv4_attention(a, D, format, stream) == hipSuccess ? DQG_OK : DQG_ERR_HIP;
   };
-  // one 16-row tile holds a token's heads; two share the decoded keys and values
-  const int nt = (long long)rows * a.r <= 16 || D > 128 ? 1 : 2;
-  if (rows <= few) return launch(nt, 0, INT_MAX, kKv4MinSteps);
+  const int few = kKv4FewRows / a.r;  // rows of a sequence that are few
+  if (force == DQG_KV4_FORCE_MANY) return launch(nt_many, 0, INT_MAX);
+  if (rows <= few || force == DQG_KV4_FORCE_FEW) return launch(nt, 0, INT_MAX);
+  const int R = 16 * nt, RM = 16 * nt_many, i = D == 64 ? 0 : D == 128 ? 1 : 2;
+  const double step_few[3] = {1.1, 1.5, 1.3}, step_many[3] = {1.3, 2.2, 2.8};  // by head dim
+  if (kv4_estimate((double)Hkv * tiles_of(R), (double)steps_of(R), kKv4MinSteps, 6.0, step_few[i], 8,
+                   4.0) <=
+      kv4_estimate((double)Hkv * tiles_of(RM), (double)steps_of(RM), kKv4MinTileSteps, 12.0,
+                   step_many[i], 2, 8.0))
+    return launch(nt, 0, INT_MAX);
   // sequences of few rows may stand among those of many: they get a launch of their own where the
   // average sequence does not fill a tile (a launch that finds none costs 4 us)
-  const bool mixed = few > 0 && B > 1 && (long long)T * a.r < (long long)B * 16 * dqg::kv4_tile_nt(D);
+  const bool mixed = few > 0 && B > 1 && (long long)T * a.r < (long long)B * RM;
   if (mixed) {
-    rc = launch(nt, 0, few, kKv4MinSteps);
+    rc = launch(nt, 0, few);
     if (rc != DQG_OK) return rc;
   }
-  return launch(dqg::kv4_tile_nt(D), mixed ? few : 0, INT_MAX, kKv4MinTileSteps);
+  return launch(nt_many, mixed ? few : 0, INT_MAX);
 }
 
 int packed_dequant_f32(const uint8_t* w, const uint16_t* s, int K, int N, int group,

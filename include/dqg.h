@@ -71,6 +71,12 @@ typedef enum dqg_format {
 #define DQG_PATH_FORCE_MFMA 0x200
 #define DQG_PATH_NO_FUSED 0x400
 
+/* Path flags, OR-ed into the `format` argument of kv4_attention (testing aid; the default, 0,
+ * picks the kernel from the sizes): every sequence on the kernel for few rows, or on the one for
+ * many. */
+#define DQG_KV4_FORCE_FEW 0x1000
+#define DQG_KV4_FORCE_MANY 0x2000
+
 /* Version of this ABI (DQG_ABI_VERSION).  Host only. */
 int dqg_abi_version(void);
 

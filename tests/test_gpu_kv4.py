@@ -189,17 +189,14 @@ def test_rows_without_a_place(fmt):
 
 # ---------------------------------------------------------------------------------------
 def run_attention(c, q, cu, lens, table, fmt, G, page, scale=None, window=0, sinks=0, split=True,
-                  hints=True, status=None, pad=0, extra=0):
-    """One call inside canary bands against the oracle."""
+                  hints=True, status=None, pad=0):
+    """The call as it picks its kernel and with each kernel forced, inside canary bands, against
+    the oracle."""
     B = _b()
     T, Hq, D = q.shape
     scale = D ** -0.5 if scale is None else scale
     want, lse, slack = K.attention(c, q, cu, lens, table, fmt, scale, window, sinks)
     n = int(cu[-1])
-    wide, check = guarded((T, Hq * D + pad), torch.bfloat16)
-    out = wide[:, :Hq * D].unflatten(1, (Hq, D))
-    lo, check_lse = guarded((T, Hq), torch.float32)
-    before, before_lse = wide.clone(), lo.clone()
     ws, check_ws = None, lambda: None
     if split:
         need = B.kv4_attention_workspace_bytes(T, len(lens), Hq, c.H, D, table.shape[1] * page)
@@ -208,24 +205,34 @@ def run_attention(c, q, cu, lens, table, fmt, G, page, scale=None, window=0, sin
     kw = {}
     if hints:
         kw = dict(max_rows=int(np.diff(cu).max()), max_kv_len=max(int(lens.max()), 1))
-    B.kv4_attention(rows_dev(q, pad), *call_where(c, cu, lens, table, fmt), c.H, page, G, fmt, scale,
-                    window=window, sinks=sinks, out=out, lse=lo, workspace=ws, status=status, **kw)
-    torch.cuda.synchronize()
-    check(), check_lse(), check_ws()
-    got, got_lse = bf16_f64(bits16(out)), lo.cpu().numpy().astype(np.float64)
-    assert np.array_equal(bits16(wide[n:]), bits16(before[n:])), "rows of nobody were written"
-    assert torch.equal(lo[n:].view(torch.int32), before_lse[n:].view(torch.int32))
+    qd, where = rows_dev(q, pad), call_where(c, cu, lens, table, fmt)
     bound, lse_bound = U.attention_bounds((want, lse), slack, D)
-    err = np.abs(got[:n] - want[:n])
-    assert int((~np.isfinite(got[:n])).sum()) == 0
-    assert np.all(err <= bound[:n]), (
-        f"{int((err > bound[:n]).sum())} of {err.size} outputs out of bounds, worst "
-        f"{float((err / bound[:n]).max())} x at {np.unravel_index(int((err / bound[:n]).argmax()), err.shape)}")
-    empty = np.isneginf(lse[:n])
-    assert np.array_equal(np.isneginf(got_lse[:n]), empty)
-    off = np.abs(np.where(empty, 0, got_lse[:n]) - np.where(empty, 0, lse[:n]))
-    over = off > np.where(empty, 0, lse_bound[:n])
-    assert not over.any(), f"{int(over.sum())} lse out of bounds, worst off by {float(off.max())}"
+    for path in (0, B.KV4_FORCE_FEW, B.KV4_FORCE_MANY):
+        wide, check = guarded((T, Hq * D + pad), torch.bfloat16)
+        out = wide[:, :Hq * D].unflatten(1, (Hq, D))
+        lo, check_lse = guarded((T, Hq), torch.float32)
+        before, before_lse = wide.clone(), lo.clone()
+        B.kv4_attention(qd, *where, c.H, page, G, fmt | path, scale, window=window, sinks=sinks,
+                        out=out, lse=lo, workspace=ws, status=status, **kw)
+        torch.cuda.synchronize()
+        check(), check_lse(), check_ws()
+        got, got_lse = bf16_f64(bits16(out)), lo.cpu().numpy().astype(np.float64)
+        assert np.array_equal(bits16(wide[n:]), bits16(before[n:])), "rows of nobody were written"
+        assert torch.equal(lo[n:].view(torch.int32), before_lse[n:].view(torch.int32))
+        err = np.abs(got[:n] - want[:n])
+        assert int((~np.isfinite(got[:n])).sum()) == 0, path
+        assert np.all(err <= bound[:n]), (
+            f"path {path:#x}: {int((err > bound[:n]).sum())} of {err.size} outputs out of bounds, "
+            f"worst {float((err / bound[:n]).max())} x at "
+            f"{np.unravel_index(int((err / bound[:n]).argmax()), err.shape)}")
+        empty = np.isneginf(lse[:n])
+        assert np.array_equal(np.isneginf(got_lse[:n]), empty)
+        off = np.abs(np.where(empty, 0, got_lse[:n]) - np.where(empty, 0, lse[:n]))
+        over = off > np.where(empty, 0, lse_bound[:n])
+        assert not over.any(), (f"path {path:#x}: {int(over.sum())} lse out of bounds, worst off by "
+                                f"{float(off.max())}")
+        if ws is not None:  # the counters are zero again, whatever the path left behind them
+            assert not ws[:2048].view(torch.int32).any()
 
 
 def attention_case(rows, lens, D, H, r, fmt, G, page, seed=0, q_scale=1.0, **kw):
@@ -315,16 +322,16 @@ def test_hidden_nan_rows_do_not_leak(fmt):
             _, ks, _, vs = c._off(0, at % page)
             c._put_scale(int(table[0, at // page]), ks if what == "k" else vs, 0x7FC0)
             q = K.bf16_value(U.bf16_bits(np.random.default_rng(1).normal(size=(n, 2, D))))
-            out = B.kv4_attention(rows_dev(q), *call_where(c, cu, lens, table, fmt), 1, page, 32, fmt,
-                                  0.125, window=window)
-            got = bf16_f64(bits16(out))
-            dirty = np.isnan(got).any(axis=(1, 2))
+            args = (rows_dev(q), *call_where(c, cu, lens, table, fmt), 1, page, 32)
             sees = np.array([p >= at and (window == 0 or at > p - window) for p in range(n)])
-            assert np.array_equal(dirty, sees), (what, window, np.nonzero(dirty != sees))
             c._put_scale(int(table[0, at // page]), ks if what == "k" else vs, 0)
             want, lse, slack = K.attention(c, q, cu, lens, table, fmt, 0.125, window)
             bound, _ = U.attention_bounds((want, lse), slack, D)
-            assert np.all(np.abs(got - want)[~sees] <= bound[~sees])
+            for path in (B.KV4_FORCE_FEW, B.KV4_FORCE_MANY):
+                got = bf16_f64(bits16(B.kv4_attention(*args, fmt | path, 0.125, window=window)))
+                dirty = np.isnan(got).any(axis=(1, 2))
+                assert np.array_equal(dirty, sees), (what, window, np.nonzero(dirty != sees))
+                assert np.all(np.abs(got - want)[~sees] <= bound[~sees])
 
 
 @pytest.mark.parametrize("fmt", FMTS)

@@ -84,6 +84,7 @@ def _attend(**kw):
 
 
 @pytest.mark.parametrize("kw,status", WHERE + [
+    (dict(fmt=B.KV4_FORCE_FEW | B.KV4_FORCE_MANY), ARG), (dict(fmt=B.KV4_FORCE_FEW | 2), UNS),
     (dict(q=0), ARG), (dict(out=0), ARG), (dict(Hq=0), ARG), (dict(Hq=30), ARG),
     (dict(scale=float("nan")), ARG), (dict(scale=float("inf")), ARG), (dict(window=-1), ARG),
     (dict(sinks=-1), ARG), (dict(rows=-1), ARG), (dict(kv=-1), ARG), (dict(qs=4088), ARG),
