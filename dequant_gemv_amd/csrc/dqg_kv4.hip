@@ -1024,6 +1024,12 @@ __global__ __launch_bounds__(64 * ROWS_WAVES, 2) void kv4_attn_rows_kernel(Kv4At
     first_round = false;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
+      // the two wavefronts of a SIMD go first in turn: left alone, the older one always does, and
+      // the other ends 4 us behind it
+      if ((i ^ (wave >> 2)) & 1)
+        __builtin_amdgcn_s_setprio(1);
+      else
+        __builtin_amdgcn_s_setprio(0);
       if (page >= 0) {
         f32x4_t sc[NT][2];
         step_scores<D, FMT, NT>(ks, q, c, sc);
@@ -1045,7 +1051,7 @@ __global__ __launch_bounds__(64 * ROWS_WAVES, 2) void kv4_attn_rows_kernel(Kv4At
   }
   if (!all_ok && lane == 0) report(a.w.status, ST_PAGE);
 
-  // join the wavefronts: sums to LDS, then each wavefront adds two rows of every 16
+  // join the wavefronts: sums to LDS, then each wavefront adds every 8th row
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float l = acc.l[nt];
@@ -1072,7 +1078,7 @@ __global__ __launch_bounds__(64 * ROWS_WAVES, 2) void kv4_attn_rows_kernel(Kv4At
     __syncthreads();
 #pragma unroll
     for (int rr = 0; rr < 16 / NW; ++rr) {
-      const int row16 = (16 / NW) * wave + rr, row = 16 * nt + row16;
+      const int row16 = wave + NW * rr, row = 16 * nt + row16;
       if (row < t.n_rho) {
         float m = lds_m[0][row];
 #pragma unroll
