@@ -67,6 +67,13 @@ __device__ __forceinline__ uint32_t pk_max_u16(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(x, y));
 }
 
+// the value of another lane: of lane ^ 1, of lane ^ 2, of the mirror image within 8 lanes, within 16
+constexpr int DPP_XOR1 = 0xB1, DPP_XOR2 = 0x4E, DPP_MIRROR8 = 0x141, DPP_MIRROR16 = 0x140;
+template <int C>
+__device__ __forceinline__ uint32_t dpp_of(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, C, 0xF, 0xF, true);
+}
+
 // ---- quantisation -----------------------------------------------------------------------
 // s = bf16(amax / c), code = nearest(x / s).  x and s have 8 significant bits, so a quotient that
 // is no tie is at least 1 / 1020 away from every tie of either grid; fma(x, 1 / s, 1536) rounds
@@ -80,18 +87,14 @@ struct GroupScale {
 template <int FMT>
 __device__ __forceinline__ GroupScale group_scale(uint32_t amax_bits) {
   GroupScale g;
-  if (amax_bits >= 0x7F80u) {  // a NaN or an infinity: the group reads back as NaN
-    g.bits = 0x7FC0u;
-    g.inv = 0.0f;
-  } else if (amax_bits < 0x0D80u) {  // below 2^-100
-    g.bits = 0;
-    g.inv = 0.0f;
-  } else {
-    const float a = __uint_as_float(amax_bits << 16);
-    // (a / c is at least 1 / 3584 of itself away from a rounding tie: the product rounds alike)
-    g.bits = f32_to_bf16(a * (FMT == FMT_INT4 ? 1.0f / 7.0f : 1.0f / 6.0f));
-    g.inv = __builtin_amdgcn_rcpf(__uint_as_float((uint32_t)g.bits << 16));
-  }
+  const float a = __uint_as_float(amax_bits << 16);
+  // (a / c is at least 1 / 3584 of itself away from a rounding tie: the product rounds alike)
+  const uint32_t bits = f32_to_bf16(a * (FMT == FMT_INT4 ? 1.0f / 7.0f : 1.0f / 6.0f));
+  const float inv = __builtin_amdgcn_rcpf(__uint_as_float(bits << 16));
+  const bool small = amax_bits < 0x0D80u;  // below 2^-100
+  const bool bad = amax_bits >= 0x7F80u;   // a NaN or an infinity: the group reads back as NaN
+  g.bits = (uint16_t)(bad ? 0x7FC0u : small ? 0u : bits);
+  g.inv = bad || small ? 0.0f : inv;
   return g;
 }
 // the code of x in the low 4 bits (INT4; the others hold rubbish)
@@ -188,7 +191,11 @@ struct Layout {
 // ---- write --------------------------------------------------------------------------------
 // K: 16 values of one position a lane (32-byte loads, 8-byte stores).  V: 2 columns of all 8
 // positions a lane, so that the lane owns whole dwords of codes; a block that the call does not
-// fill keeps the other positions' nibbles.
+// fill keeps the other positions' nibbles.  A wavefront takes K or V of one block and head: the
+// most wavefronts, for a single row as for a prompt.
+// Instructions bound it, not memory (per wavefront about 250 for K, 450 for V and 2 KB of rows):
+// maxima cross lanes by DPP, loads and scales are free of branches.  3 times 5001 rows of 4 heads
+// of 128: 10.2 us (39 MB: 3.8 TB/s, of the 5.1 of a large copy); one row: 3.6 us.
 template <int D, int FMT>
 __global__ __launch_bounds__(256) void kv4_write_kernel(Kv4RowsArgs a, int n_units) {
   const int unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -218,10 +225,10 @@ __global__ __launch_bounds__(256) void kv4_write_kernel(Kv4RowsArgs a, int n_uni
 #pragma unroll
       for (int i = 0; i < 8; ++i) m = pk_max_u16(m, u[i] & 0x7FFF7FFFu);
       uint32_t am = max(m & 0xFFFFu, m >> 16);
-      am = max(am, (uint32_t)__shfl_xor((int)am, 1));
+      am = max(am, dpp_of<DPP_XOR1>(am));
       if (gs == 7) {
-        am = max(am, (uint32_t)__shfl_xor((int)am, 2));
-        am = max(am, (uint32_t)__shfl_xor((int)am, 4));
+        am = max(am, dpp_of<DPP_XOR2>(am));
+        am = max(am, dpp_of<DPP_MIRROR8>(am));
       }
       const GroupScale g = group_scale<FMT>(am);
       uint32_t c[2];
@@ -247,24 +254,26 @@ __global__ __launch_bounds__(256) void kv4_write_kernel(Kv4RowsArgs a, int n_uni
   } else {
 #pragma unroll
     for (int it = 0; it < (D + 127) / 128; ++it) {
-      const int d0 = it * 128 + 2 * lane;
-      const bool mine = d0 < D;
+      const bool mine = it * 128 + 2 * lane < D;
+      const int d0 = mine ? it * 128 + 2 * lane : 0;
       uint32_t u[8];
+      const uint16_t* row = a.v + (o.row + o.lo) * a.v_stride + (int64_t)o.head * D;
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        u[t] = 0;
-        if (mine && t >= o.lo && t < o.hi)
-          u[t] = *reinterpret_cast<const uint32_t*>(a.v + (o.row + t) * a.v_stride +
-                                                    (int64_t)o.head * D + d0);
+      for (int t = 0; t < 8; ++t) {  // (a position that is not the call's: the nearest that is)
+        if (t > 0) row += t > o.lo && t < o.hi ? a.v_stride : 0;
+        u[t] = *reinterpret_cast<const uint32_t*>(row + (uint32_t)d0);
       }
+      const bool whole = o.lo == 0 && o.hi == 8;
       float inv[8];
       uint16_t bits[8];
 #pragma unroll
       for (int t = 0; t < 8; t += 2) {  // two positions' maxima in one dword
         const uint32_t x = u[t] & 0x7FFF7FFFu, y = u[t + 1] & 0x7FFF7FFFu;
         uint32_t m = max(x & 0xFFFFu, x >> 16) | (max(y & 0xFFFFu, y >> 16) << 16);
-#pragma unroll
-        for (int k = 1; k < 16; k *= 2) m = pk_max_u16(m, (uint32_t)__shfl_xor((int)m, k));
+        m = pk_max_u16(m, dpp_of<DPP_XOR1>(m));
+        m = pk_max_u16(m, dpp_of<DPP_XOR2>(m));
+        m = pk_max_u16(m, dpp_of<DPP_MIRROR8>(m));
+        m = pk_max_u16(m, dpp_of<DPP_MIRROR16>(m));
         if (gs == 7) {
           m = pk_max_u16(m, (uint32_t)__shfl_xor((int)m, 16));
           m = pk_max_u16(m, (uint32_t)__shfl_xor((int)m, 32));
@@ -282,7 +291,6 @@ __global__ __launch_bounds__(256) void kv4_write_kernel(Kv4RowsArgs a, int n_uni
       uint2 c = make_uint2(encode8<FMT>(f0, inv), encode8<FMT>(f1, inv));
       if (mine) {
         uint2* p = reinterpret_cast<uint2*>(o.base + L.vc + ((o.slot >> 3) * D + d0) * 4);
-        const bool whole = o.lo == 0 && o.hi == 8;
         if (!whole) {
           const uint32_t keep = ~(uint32_t)((((uint64_t)1 << (4 * o.hi)) - 1) &
                                             ~(((uint64_t)1 << (4 * o.lo)) - 1));
@@ -294,9 +302,18 @@ __global__ __launch_bounds__(256) void kv4_write_kernel(Kv4RowsArgs a, int n_uni
         if ((d0 & ((1 << gs) - 1)) == 0) {
           uint16_t* s = reinterpret_cast<uint16_t*>(
               o.base + L.vs + 16 * (((o.slot >> 3) << L.n_shift) + (d0 >> gs)));
+          if (whole) {
+            uint4 w;
+            w.x = bits[0] | (uint32_t)bits[1] << 16;
+            w.y = bits[2] | (uint32_t)bits[3] << 16;
+            w.z = bits[4] | (uint32_t)bits[5] << 16;
+            w.w = bits[6] | (uint32_t)bits[7] << 16;
+            *reinterpret_cast<uint4*>(s) = w;
+          } else {
 #pragma unroll
-          for (int t = 0; t < 8; ++t)
-            if (t >= o.lo && t < o.hi) s[t] = bits[t];
+            for (int t = 0; t < 8; ++t)
+              if (t >= o.lo && t < o.hi) s[t] = bits[t];
+          }
         }
       }
     }
@@ -305,7 +322,8 @@ __global__ __launch_bounds__(256) void kv4_write_kernel(Kv4RowsArgs a, int n_uni
 
 // ---- read ---------------------------------------------------------------------------------
 // The same lanes the other way round.  Rows without a place in the cache (before position 0, or
-// behind the table, or in a page that is not there) read as zeros.
+// behind the table, or in a page that is not there) read as zeros.  Bound by memory: 32768 rows of
+// 4 heads of 128 17.0 us (86 MB: 5.1 TB/s, as a large copy); the 15003 rows above 9.4 us.
 template <int D, int FMT>
 __global__ __launch_bounds__(256) void kv4_read_kernel(Kv4RowsArgs a, int n_units) {
   const int unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -317,13 +335,14 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(Kv4RowsArgs a, int n_unit
   if (!block_at(a.w, hs / a.w.Hkv, hs % a.w.Hkv, o)) return;
   const Layout<D> L(a.w);
   const int gs = a.w.group_shift;
+  constexpr uint32_t zeros = FMT == FMT_INT4 ? 0x88888888u : 0u;  // codes of 0
   if (!is_v) {
     constexpr int LT = D / 16;
 #pragma unroll
     for (int it = 0; it < (8 * LT + 63) / 64; ++it) {
       const int item = it * 64 + lane, t = item / LT, d0 = (item % LT) * 16;
       if (t < o.lo || t >= o.hi) continue;
-      uint2 c = make_uint2(0, 0);
+      uint2 c = make_uint2(zeros, zeros);
       float s = 0.0f;
       if (o.held) {
         c = *reinterpret_cast<const uint2*>(o.base + (o.slot + t) * (D / 2) + d0 / 2);
@@ -337,8 +356,8 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(Kv4RowsArgs a, int n_unit
         decode8<FMT>(c.y, y);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          f[i] = o.held ? x[i] * s : 0.0f;
-          f[8 + i] = o.held ? y[i] * s : 0.0f;
+          f[i] = x[i] * s;
+          f[8 + i] = y[i] * s;
         }
       }
       uint32_t r[8];
@@ -357,7 +376,7 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(Kv4RowsArgs a, int n_unit
     for (int it = 0; it < (D + 127) / 128; ++it) {
       const int d0 = it * 128 + 2 * lane;
       if (d0 >= D) continue;
-      uint2 c = make_uint2(0, 0);
+      uint2 c = make_uint2(zeros, zeros);
       uint4 sv = make_uint4(0, 0, 0, 0);
       if (o.held) {
         c = *reinterpret_cast<const uint2*>(o.base + L.vc + ((o.slot >> 3) * D + d0) * 4);
@@ -368,14 +387,23 @@ __global__ __launch_bounds__(256) void kv4_read_kernel(Kv4RowsArgs a, int n_unit
       float x[8], y[8];
       decode8<FMT>(c.x, x);
       decode8<FMT>(c.y, y);
+      uint32_t h[8];
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
-        if (t < o.lo || t >= o.hi) continue;
         const float s = (t & 1) ? bf16_hi(sw[t / 2]) : bf16_lo(sw[t / 2]);
-        const bf16x2_t h = {(__bf16)(o.held ? x[t] * s : 0.0f),
-                            (__bf16)(o.held ? y[t] * s : 0.0f)};
-        *reinterpret_cast<uint32_t*>(a.v_out + (o.row + t) * a.v_stride + (int64_t)o.head * D + d0) =
-            __builtin_bit_cast(uint32_t, h);
+        const bf16x2_t z = {(__bf16)(x[t] * s), (__bf16)(y[t] * s)};
+        h[t] = __builtin_bit_cast(uint32_t, z);
+      }
+      uint16_t* row = a.v_out + (o.row + o.lo) * a.v_stride + (int64_t)o.head * D;
+      if (o.lo == 0 && o.hi == 8) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t, row += a.v_stride)
+          *reinterpret_cast<uint32_t*>(row + (uint32_t)d0) = h[t];
+      } else {
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+          if (t >= o.lo && t < o.hi)
+            *reinterpret_cast<uint32_t*>(row + (t - o.lo) * a.v_stride + d0) = h[t];
       }
     }
   }
