@@ -1165,7 +1165,9 @@ __global__ __launch_bounds__(64 * ROWS_WAVES, 2) void kv4_attn_rows_kernel(Kv4At
 // Wavefronts 0-3 (group 0) and 4-7 (group 1), one of each on every SIMD, do a turn's work in
 // different orders, so that one has matrix instructions while the other has arithmetic.
 // D <= 128, one barrier a turn (two buffers of K and of V): group 0 takes scores, weights, outputs,
-// decoding of the next turn; group 1 starts with the decoding.
+// decoding of the next turn; group 1 starts with the decoding.  Weights with outputs, and group 1's
+// decoding, go before the other wavefront's instructions (causal prompts of 2 times 4096 rows: 252
+// us; 272 without, and with either of the two alone).
 // D = 256: two phases with a barrier behind each: M, the matrix instructions (S of this turn, O of
 // the turn before), and A, the arithmetic (weights of this turn, decoding).  Slot 2 t (between two
 // barriers) is phase M of turn t for group 0 and phase A of turn t - 1 for group 1, slot 2 t + 1 the
@@ -1527,40 +1529,39 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
   float m = -FLT_MAX, l = 0.0f;  // m: of the scores before scaling
   // hides what the rows do not see of a turn's scores; the lane's largest score
   const auto mask_scores = [&](int turn) {
-    float mx;
-              const int i0 = s0 + 2 * turn + (HV == 2 ? half : 0) - list0;
-              constexpr uint64_t UM = (1u << NU) - 1;
-              if ((edges >> i0) & UM) {
-    #pragma unroll
-                for (int u = 0; u < NU; ++u) {
-                  uint32_t bad = 0;
-                  if ((edges >> (i0 + u)) & 1)
-    #pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                      bad |= lds_bad[turn & 3][4 * (HV == 2 ? half : u) + b] << (8 * b);
-                  if (!((my_edges >> (i0 + u)) & 1) && bad == 0) continue;
-                  const int t0 = __builtin_amdgcn_readlane(l_pos, i0 + u);
-                  // against the constant offset of a register's position
-                  const int to = pos - t0 - 8 * h, from = a.window > 0 ? to - a.window : -1000;
-                  const int first = a.sinks - t0 - 8 * h;
-    #pragma unroll
-                  for (int i = 0; i < 16; ++i) {
-                    const int at = 16 * (i >> 3) + (i & 7);
-                    const bool seen = at <= to && (at > from || at < first);
-                    sc[u][i] = seen ? sc[u][i] : -INFINITY;
-                  }
-                  if (bad) {
-                    const uint32_t mine = bad >> (8 * h);
-    #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                      if ((mine >> (16 * (i >> 3) + (i & 7))) & 1 && sc[u][i] != -INFINITY)
-                        sc[u][i] = NAN;
-                  }
-                }
-              }
-              mx = fmaxf(sc[0][0], sc[NU - 1][0]);
-    #pragma unroll
-              for (int i = 1; i < 16; ++i) mx = fmaxf(fmaxf(mx, sc[0][i]), sc[NU - 1][i]);
+    const int i0 = s0 + 2 * turn + (HV == 2 ? half : 0) - list0;
+    constexpr uint64_t UM = (1u << NU) - 1;
+    if ((edges >> i0) & UM) {
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        uint32_t bad = 0;
+        if ((edges >> (i0 + u)) & 1)
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            bad |= lds_bad[turn & 3][4 * (HV == 2 ? half : u) + b] << (8 * b);
+        if (!((my_edges >> (i0 + u)) & 1) && bad == 0) continue;
+        const int t0 = __builtin_amdgcn_readlane(l_pos, i0 + u);
+        // against the constant offset of a register's position
+        const int to = pos - t0 - 8 * h, from = a.window > 0 ? to - a.window : -1000;
+        const int first = a.sinks - t0 - 8 * h;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int at = 16 * (i >> 3) + (i & 7);
+          const bool seen = at <= to && (at > from || at < first);
+          sc[u][i] = seen ? sc[u][i] : -INFINITY;
+        }
+        if (bad) {
+          const uint32_t mine = bad >> (8 * h);
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if ((mine >> (16 * (i >> 3) + (i & 7))) & 1 && sc[u][i] != -INFINITY)
+              sc[u][i] = NAN;
+        }
+      }
+    }
+    float mx = fmaxf(sc[0][0], sc[NU - 1][0]);
+#pragma unroll
+    for (int i = 1; i < 16; ++i) mx = fmaxf(fmaxf(mx, sc[0][i]), sc[NU - 1][i]);
     return mx;
   };
   const auto move_reference = [&](float mx) {  // mx: of the row
@@ -1605,10 +1606,14 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
       __syncthreads();
 #pragma unroll 1
       for (int turn = 0; turn < n_turns; ++turn) {
+        __builtin_amdgcn_s_setprio(1);
         if (group == 1) decode_next(turn + 1);
+        __builtin_amdgcn_s_setprio(0);
         tile_scores<D, NU>(&lds_k[turn & 1][h][k_tok], q, sc);
         const float ref = move_reference(mask_scores(turn));
+        __builtin_amdgcn_s_setprio(1);
         tile_values<D, NJ>(&lds_v[turn & 1][h][q32], [&](int b) { return weights(b, ref); }, o);
+        __builtin_amdgcn_s_setprio(0);
         if (group == 0) decode_next(turn + 1);
         __syncthreads();
       }
