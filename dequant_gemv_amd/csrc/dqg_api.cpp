@@ -323,8 +323,14 @@ inline int log2_of(int v) { return 31 - __builtin_clz((unsigned)v); }
 // parts of a head's steps: as many as run at once
 int kv4_parts(int Hkv) { return std::max(kKv4Resident / Hkv, 1); }
 // A tile that is cut has more than `per` steps and per >= (all steps) / parts, so there are at most
-// `parts` such tiles and 2 parts pieces of them: [counters][partials], 2 parts of each.
-size_t kv4_counter_bytes(int Hkv) { return up256(sizeof(unsigned) * 2 * Hkv * kv4_parts(Hkv)); }
+// `parts` such tiles and 2 parts pieces of them.  Workspace: [counters][partials, 2 parts of each
+// head][plan].  The counters, zero between calls, have the same room for any Hkv, so that calls of
+// different sizes may share a workspace.
+constexpr size_t kKv4CounterBytes = sizeof(unsigned) * 2 * std::max(kKv4Resident, kKv4MaxHeads);
+size_t kv4_partial_bytes(int Hkv, int D) {
+  return up256(2 * (size_t)Hkv * kv4_parts(Hkv) * sizeof(float) *
+               dqg::kv4_part_floats(dqg::kv4_tile_nt(D), D));
+}
 long long kv4_steps(long long positions) {
   return (positions + dqg::KV4_STEP - 1) / dqg::KV4_STEP;
 }
@@ -722,8 +728,8 @@ int kv4_read(uint16_t* k, uint16_t* v, int T, int64_t k_stride, int64_t v_stride
 size_t kv4_attention_workspace_bytes(int T, int B, int Hq, int Hkv, int D, int max_kv_len) {
   if (!kv4_attn_sizes_ok(T, B, Hq, Hkv, D) || max_kv_len < 1 || max_kv_len > (1 << 30)) return 0;
   if (max_kv_len <= kKv4MinSteps * dqg::KV4_STEP) return 0;
-  return up256(kv4_counter_bytes(Hkv) + 2 * (size_t)Hkv * kv4_parts(Hkv) * sizeof(float) *
-                                         dqg::kv4_part_floats(dqg::kv4_tile_nt(D), D));
+  return kKv4CounterBytes + kv4_partial_bytes(Hkv, D) +
+         (B > 64 ? up256(sizeof(int2) * ((size_t)B + 1)) : 0);
 }
 
 int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32_t* cu_rows,
@@ -749,13 +755,16 @@ int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32
   if (workspace && !aligned16(workspace)) return DQG_ERR_MISALIGNED;
   const int cap = max_pages * page_size;
   const int most = max_kv_len ? std::min(max_kv_len, cap) : cap;
-  if (workspace && workspace_bytes < kv4_attention_workspace_bytes(T, B, Hq, Hkv, D, most))
-    return DQG_ERR_WORKSPACE;
+  const size_t need = kv4_attention_workspace_bytes(T, B, Hq, Hkv, D, most);
+  if (workspace && workspace_bytes < need) return DQG_ERR_WORKSPACE;
   dqg::Kv4AttnArgs a{};
   a.w = kv4_where(T, B, cu_rows, kv_lens, block_table, max_pages, cache, num_pages, Hkv, D,
                   page_size, group, status);
   a.q = q; a.q_stride = q_stride; a.out = out; a.out_stride = out_stride; a.lse = lse;
-  a.Hq = Hq; a.r = Hq / Hkv; a.scale = scale; a.window = window; a.sinks = sinks;
+  a.Hq = Hq; a.r = Hq / Hkv; a.scale = scale;
+  // (positions end below 2^30: larger ones are the same, and sums with them stay in 32 bits)
+  a.window = std::min(window, 1 << 30);
+  a.sinks = std::min(sinks, 1 << 30);
   a.r_shift = a.r > 1 ? 32 - __builtin_clz((unsigned)(a.r - 1)) : 0;
   a.r_mul = (uint32_t)(((1ull << 32) * ((1ull << a.r_shift) - a.r)) / a.r + 1);
   const int rows = std::max(std::min(max_rows ? max_rows : T, T), (T + B - 1) / B);
@@ -782,10 +791,13 @@ int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32
     // sum of ceil(n r / R) over the sequences; pieces are at most tiles + parts
     const long long tiles = (long long)T * a.r / R + B;
     // places in a batch's steps are 32-bit
-    const bool cut = workspace && tiles * (cap / dqg::KV4_STEP) < (1LL << 30);
-    a.counters = cut ? static_cast<unsigned*>(workspace) : nullptr;
-    a.part = cut ? reinterpret_cast<float*>(static_cast<char*>(workspace) + kv4_counter_bytes(Hkv))
-                 : nullptr;
+    // (need 0: the workspace may have any size)
+    const bool cut = workspace && need && tiles * (cap / dqg::KV4_STEP) < (1LL << 30);
+    char* const ws = static_cast<char*>(workspace);
+    a.counters = cut ? reinterpret_cast<unsigned*>(ws) : nullptr;
+    a.part = cut ? reinterpret_cast<float*>(ws + kKv4CounterBytes) : nullptr;
+    a.plan = cut && B > 64 ? reinterpret_cast<int2*>(ws + kKv4CounterBytes + kv4_partial_bytes(Hkv, D))
+                           : nullptr;
     a.n_groups = (int)(tiles + (cut ? a.n_parts : 0));
     if ((long long)a.n_groups * Hkv >= (1LL << 31)) return DQG_ERR_UNSUPPORTED;
     return dqg::launch_kv4_attention(a, D, format, stream) == hipSuccess ? DQG_OK : DQG_ERR_HIP;

@@ -152,6 +152,7 @@ struct Kv4AttnArgs {
   float* lse;            // [T, Hq] or null
   float* part;           // partial sums [Hkv][2 n_parts]; null: tiles are not cut
   unsigned* counters;    // [Hkv][2 n_parts], zero between calls
+  int2* plan;            // [B + 1] of the launch, where tiles are cut and B > 64; else null
   int Hq, r;             // query heads, and query heads per kv head
   uint32_t r_mul;        // division by r (see row_of)
   int r_shift;

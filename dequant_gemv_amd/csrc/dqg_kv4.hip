@@ -31,21 +31,25 @@ __device__ __forceinline__ void report(int* status, int bit) {
   if (status) atomicOr(status, bit);
 }
 
-// The sequence that slot `slot` falls to when sequence b's slots start at first(cu[b]) + b * per:
-// the count of sequences that start at or before it, 64 a step.  Uniform over the wavefront.
+// The last i of 0 .. n - 1 with key(i) <= x, where key ascends from key(0) <= x: 64 candidates a
+// step.  Uniform over the wavefront; in range for any keys.
+template <class F>
+__device__ __forceinline__ int last_at_most(int n, int x, F key) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, end = n;
+  while (end - lo > 1) {
+    const int step = (end - lo + 63) >> 6, i = lo + lane * step;
+    const int c = __popcll(__ballot(i < end && key(i) <= x));
+    lo += max(c - 1, 0) * step;
+    end = min(lo + step, end);
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+// The sequence that slot `slot` falls to when sequence b's slots start at first(cu[b]) + b * per.
 template <class F>
 __device__ __forceinline__ int seq_of_slot(const Kv4Where& w, int slot, int per, F first) {
-  const int lane = threadIdx.x & 63;
-  int n = 0;
-  for (int b0 = 0; b0 < w.B; b0 += 64) {
-    const int b = b0 + lane;
-    bool at = false;
-    if (b < w.B) at = first(min(max(w.cu[b], 0), w.T)) + b * per <= slot;
-    const int c = __popcll(__ballot(at));
-    n += c;
-    if (c < 64) break;
-  }
-  return max(__builtin_amdgcn_readfirstlane(n) - 1, 0);
+  return last_at_most(w.B, slot,
+                      [&](int b) { return first(min(max(w.cu[b], 0), w.T)) + b * per; });
 }
 
 struct Seq {
@@ -804,30 +808,14 @@ __device__ __forceinline__ void seq_work(const Kv4AttnArgs& a, const Seq& s, int
   }
   *steps = max(w, 1);
 }
-// 64 sequences, one a lane: their tiles, the steps of a tile, and how a tile is cut.
-struct Lanes {
-  int tiles, steps, chunk, k;  // k pieces of chunk steps, the last may be shorter
-  Seq s;
-};
-__device__ __forceinline__ void load_lanes(const Kv4AttnArgs& a, int R, int b0, Lanes& c) {
-  const int b = b0 + (threadIdx.x & 63);
-  c.tiles = 0;
-  c.steps = 1;
-  c.s = Seq{0, 0, 0, 0};
-  if (b < a.w.B) {
-    c.s = seq_at(a.w, b);
-    seq_work(a, c.s, R, &c.tiles, &c.steps);
-  }
-}
-__device__ __forceinline__ void cut_lanes(const Kv4AttnArgs& a, int per, Lanes& c) {
-  c.chunk = c.steps;
-  c.k = 1;
-  if (c.steps > per && c.steps > 2 * a.min_steps) {
-    const unsigned k = ((unsigned)c.steps + per - 1) / (unsigned)per;
-    // multiples of 8: a step more costs a wavefront of 8 as much as 8
-    c.chunk = (int)(((unsigned)c.steps + k - 1) / k + 7) & ~7;
-    c.k = (int)(((unsigned)c.steps + c.chunk - 1) / (unsigned)c.chunk);
-  }
+// Pieces of a tile of `steps` steps, of *chunk steps each; the last may be shorter.
+__device__ __forceinline__ int cut_steps(const Kv4AttnArgs& a, int steps, int per, int* chunk) {
+  *chunk = steps;
+  if (steps <= per || steps <= 2 * a.min_steps) return 1;
+  const unsigned k = ((unsigned)steps + per - 1) / (unsigned)per;
+  // multiples of 8: a step more costs a wavefront of 8 as much as 8
+  *chunk = (int)(((unsigned)steps + k - 1) / k + 7) & ~7;
+  return (int)(((unsigned)steps + *chunk - 1) / (unsigned)*chunk);
 }
 __device__ __forceinline__ int wave_total(int v) {
   return __builtin_amdgcn_readlane(wave_incl_sum(v), 63);
@@ -840,73 +828,131 @@ struct Piece {
   int n, index;    // pieces of the tile, and which of them this is
   int partial;     // where its partial sums go, in units of partials
 };
-// The x-th piece, from the last; false: there are not as many.  Uniform over the workgroup.
+// at: the piece's place among those of sequence f.b, which has `tiles` tiles cut into f.n pieces
+__device__ __forceinline__ bool set_piece(const Kv4AttnArgs& a, int at, int tiles, int steps,
+                                          int chunk, Piece& f) {
+  f.tile = f.n > 1 ? at / f.n : at;
+  f.index = at - f.tile * f.n;
+  f.s0 = f.index * chunk;
+  f.s1 = min(f.s0 + chunk, steps);
+  // (always so for cu_rows that ascend)
+  return f.tile >= 0 && f.tile < tiles && (f.n == 1 || (unsigned)f.partial < 2u * a.n_parts);
+}
+// The x-th piece, from the last (the pieces of later tiles, which see more, first); false: there
+// are not as many.  Uniform over the workgroup.
+// Up to 64 sequences: one a lane.  More: from the plan that a kernel before this one has made (as
+// many loads as a search needs, where every workgroup would go through the whole batch), or,
+// where nothing is cut, by slots: floor(cu[b + 1] r / R) - floor(cu[b] r / R) + 1 are enough for
+// the tiles of sequence b.
 __device__ __forceinline__ bool find_piece(const Kv4AttnArgs& a, int R, int x, Piece& f) {
-  Lanes c;
-  load_lanes(a, R, 0, c);
+  int tiles, steps, chunk;
+  if (a.w.B > 64) {
+    int at;
+    if (a.plan) {
+      const int2 all = a.plan[a.w.B];
+      x = all.x - 1 - x;
+      if (x < 0) return false;
+      f.b = last_at_most(a.w.B, x, [&](int b) { return a.plan[b].x; });
+      const int2 before = a.plan[f.b];
+      f.s = seq_at(a.w, f.b);
+      seq_work(a, f.s, R, &tiles, &steps);
+      f.n = cut_steps(a, steps, all.y, &chunk);
+      at = x - before.x;
+      f.partial = before.y + at;
+    } else {
+      const auto slots = [&](int c) { return c * a.r / R; };
+      x = a.n_groups - 1 - x;
+      f.b = seq_of_slot(a.w, x, 1, slots);
+      f.s = seq_at(a.w, f.b);
+      seq_work(a, f.s, R, &tiles, &steps);
+      f.n = 1;
+      chunk = steps;
+      at = x - (slots(f.s.row0) + f.b);
+      f.partial = 0;
+    }
+    return set_piece(a, at, tiles, steps, chunk, f);
+  }
+  const int b = threadIdx.x & 63;
+  Seq s{0, 0, 0, 0};
+  tiles = 0;
+  steps = 1;
+  if (b < a.w.B) {
+    s = seq_at(a.w, b);
+    seq_work(a, s, R, &tiles, &steps);
+  }
   int per = 1 << 30;
   if (a.part) {
-    int total = wave_total(c.tiles * c.steps), tiles = wave_total(c.tiles);
-    if (a.w.B > 64) {
-      for (int b0 = 64; b0 < a.w.B; b0 += 64) {
-        Lanes d;
-        load_lanes(a, R, b0, d);
-        total += wave_total(d.tiles * d.steps);
-      }
-      tiles = 0;
-    }
-    per = max((total + a.n_parts - 1) / a.n_parts, a.min_steps);
-    if (a.w.B <= 64) {
-      const int most = max(a.n_parts, tiles);
-      while (true) {
-        const float r = __builtin_amdgcn_rcpf((float)per);
-        if (wave_total(c.tiles * max((int)ceilf((float)c.steps * r - 1e-3f), 1)) <= most) break;
-        per += (per >> 3) + 1;
-      }
+    const int most = max(a.n_parts, wave_total(tiles));
+    per = max((wave_total(tiles * steps) + a.n_parts - 1) / a.n_parts, a.min_steps);
+    while (true) {
+      const float r = __builtin_amdgcn_rcpf((float)per);
+      if (wave_total(tiles * max((int)ceilf((float)steps * r - 1e-3f), 1)) <= most) break;
+      per += (per >> 3) + 1;
     }
   }
-  int pieces = 0, cuts = 0, n_pieces = 0;
-  cut_lanes(a, per, c);
-  if (a.w.B <= 64) {
-    n_pieces = wave_total(c.tiles * c.k);
-  } else {
-    for (int b0 = 0; b0 < a.w.B; b0 += 64) {
-      Lanes d;
-      load_lanes(a, R, b0, d);
-      cut_lanes(a, per, d);
-      n_pieces += wave_total(d.tiles * d.k);
-    }
-  }
-  x = n_pieces - 1 - x;  // the pieces of later tiles, which see more, first
+  const int k = cut_steps(a, steps, per, &chunk), mine = tiles * k, cut = k > 1 ? mine : 0;
+  const int incl = wave_incl_sum(mine), cincl = wave_incl_sum(cut);
+  x = __builtin_amdgcn_readlane(incl, 63) - 1 - x;
   if (x < 0) return false;
-  int b0 = 0;
-  while (true) {
-    const int mine = c.tiles * c.k, cut = c.k > 1 ? mine : 0;
-    const int incl = wave_incl_sum(mine), cincl = wave_incl_sum(cut);
-    const int all = __builtin_amdgcn_readlane(incl, 63);
-    if (x < pieces + all || b0 + 64 >= a.w.B) {
-      const int i = min(__popcll(__ballot(pieces + incl <= x)), 63);
-      const int at = x - (pieces + __builtin_amdgcn_readlane(incl - mine, i));
-      f.b = b0 + i;
-      f.n = __builtin_amdgcn_readlane(c.k, i);
-      f.tile = f.n > 1 ? at / f.n : at;
-      f.index = at - f.tile * f.n;
-      const int chunk = __builtin_amdgcn_readlane(c.chunk, i);
-      f.s0 = f.index * chunk;
-      f.s1 = min(f.s0 + chunk, __builtin_amdgcn_readlane(c.steps, i));
-      f.partial = cuts + __builtin_amdgcn_readlane(cincl - cut, i) + at;
-      f.s.row0 = __builtin_amdgcn_readlane(c.s.row0, i);
-      f.s.n = __builtin_amdgcn_readlane(c.s.n, i);
-      f.s.len = __builtin_amdgcn_readlane(c.s.len, i);
-      f.s.cap = __builtin_amdgcn_readlane(c.s.cap, i);
-      return true;
+  f.b = min(__popcll(__ballot(incl <= x)), 63);
+  const int at = x - __builtin_amdgcn_readlane(incl - mine, f.b);
+  f.n = __builtin_amdgcn_readlane(k, f.b);
+  f.partial = __builtin_amdgcn_readlane(cincl - cut, f.b) + at;
+  f.s.row0 = __builtin_amdgcn_readlane(s.row0, f.b);
+  f.s.n = __builtin_amdgcn_readlane(s.n, f.b);
+  f.s.len = __builtin_amdgcn_readlane(s.len, f.b);
+  f.s.cap = __builtin_amdgcn_readlane(s.cap, f.b);
+  return set_piece(a, at, __builtin_amdgcn_readlane(tiles, f.b),
+                   __builtin_amdgcn_readlane(steps, f.b), __builtin_amdgcn_readlane(chunk, f.b), f);
+}
+
+// The plan of a batch of more than 64 sequences: for each the pieces, and the pieces of cut tiles,
+// before its own; behind them all pieces, and the steps of a piece.  One workgroup.
+constexpr int PLAN_THREADS = 1024;
+__global__ __launch_bounds__(PLAN_THREADS) void kv4_plan_kernel(Kv4AttnArgs a, int R) {
+  __shared__ int sums[2][PLAN_THREADS / 64];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // sums over the threads before this one, and over all
+  const auto scan = [&](int x, int y, int2& before, int2& all) {
+    const int ix = wave_incl_sum(x), iy = wave_incl_sum(y);
+    __syncthreads();
+    if (lane == 63) {
+      sums[0][wave] = ix;
+      sums[1][wave] = iy;
     }
-    pieces += all;
-    cuts += __builtin_amdgcn_readlane(cincl, 63);
-    b0 += 64;
-    load_lanes(a, R, b0, c);
-    cut_lanes(a, per, c);
+    __syncthreads();
+    before = make_int2(ix - x, iy - y);
+    all = make_int2(0, 0);
+    for (int w = 0; w < PLAN_THREADS / 64; ++w) {
+      before.x += w < wave ? sums[0][w] : 0;
+      before.y += w < wave ? sums[1][w] : 0;
+      all.x += sums[0][w];
+      all.y += sums[1][w];
+    }
+  };
+  int total = 0, tiles, steps, chunk;
+  for (int b = tid; b < a.w.B; b += PLAN_THREADS) {
+    seq_work(a, seq_at(a.w, b), R, &tiles, &steps);
+    total += tiles * steps;
   }
+  int2 before, all, done = make_int2(0, 0);
+  scan(total, 0, before, all);
+  const int per = max((all.x + a.n_parts - 1) / a.n_parts, a.min_steps);
+  for (int b0 = 0; b0 < a.w.B; b0 += PLAN_THREADS) {
+    const int b = b0 + tid;
+    int mine = 0, cut = 0;
+    if (b < a.w.B) {
+      seq_work(a, seq_at(a.w, b), R, &tiles, &steps);
+      const int k = cut_steps(a, steps, per, &chunk);
+      mine = tiles * k;
+      cut = k > 1 ? mine : 0;
+    }
+    scan(mine, cut, before, all);
+    if (b < a.w.B) a.plan[b] = make_int2(done.x + before.x, done.y + before.y);
+    done.x += all.x;
+    done.y += all.y;
+  }
+  if (tid == 0) a.plan[a.w.B] = make_int2(done.x, per);
 }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t part_rsrc(const float* p) {
@@ -1542,7 +1588,7 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
         if (!((my_edges >> (i0 + u)) & 1) && bad == 0) continue;
         const int t0 = __builtin_amdgcn_readlane(l_pos, i0 + u);
         // against the constant offset of a register's position
-        const int to = pos - t0 - 8 * h, from = a.window > 0 ? to - a.window : -1000;
+        const int to = pos - t0 - 8 * h, from = a.window > 0 ? max(to, -1) - a.window : -1000;
         const int first = a.sinks - t0 - 8 * h;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -1728,6 +1774,11 @@ hipError_t launch_rows(const Kv4RowsArgs& a, hipStream_t st) {
 template <int D, int FMT>
 hipError_t launch_attn(const Kv4AttnArgs& a, hipStream_t st) {
   const unsigned grid = (unsigned)a.w.Hkv * a.n_groups;
+  if (a.plan) {
+    kv4_plan_kernel<<<1, PLAN_THREADS, 0, st>>>(a, 16 * a.nt);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   if (a.nt == kv4_tile_nt(D)) {
     kv4_attn_tiles_kernel<D, FMT><<<grid, TILE_THREADS, 0, st>>>(a);
     return hipGetLastError();
