@@ -779,12 +779,20 @@ int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32
   };
   // one 16-row tile holds a token's heads; two share the decoded keys and values
   const int nt = (long long)rows * a.r <= 16 || D > 128 ? 1 : 2, nt_many = dqg::kv4_tile_nt(D);
+  // Few rows, many tiles: workgroups of 4 wavefronts, of which 2 or 3 share a compute unit, so that
+  // one loads while another starts or ends.  Tokens of 4 heads of a kv head, 8 or 4 wavefronts:
+  // heads of 128, 512 tiles of up to 300 positions 12.2 and 9.6 us, of up to 2800 39.1 and 35.6; 768
+  // tiles 21.5 and 14.9, 57.7 and 51.3; 8192 of up to 1400 321 and 226.  With fewer, long caches
+  // need all wavefronts of a compute unit on one tile (264 tiles of up to 2800 26.5 and 32.1).
+  // Heads of 64, whose workgroups of 8 share a compute unit too: 512 tiles of up to 2800 23.3 and
+  // 27.0, 768 40.2 and 37.7.
   const auto launch = [&](int tiles16, int over, int to) -> int {
     const int R = 16 * tiles16, min_steps = tiles16 == nt_many ? kKv4MinTileSteps : kKv4MinSteps;
     a.nt = tiles16;
     a.rows_over = over;
     a.rows_to = to;
     a.min_steps = min_steps;
+    a.waves = Hkv * tiles_of(R) >= (D == 64 ? 3 : 2) * kKv4Resident ? 4 : 8;
     // (hints may be wrong: any n_parts gives the right result)
     a.n_parts = (int)std::max(1LL, std::min<long long>(kv4_parts(Hkv), (tiles_of(R) * steps_of(R) + min_steps - 1) /
                                                                            min_steps));

@@ -162,6 +162,7 @@ struct Kv4AttnArgs {
   int n_groups;          // workgroups of a head: at least as many as pieces
   int min_steps;         // steps of a piece, at least
   int nt;                // 16-row tiles per workgroup: 1, 2 or kv4_tile_nt(D)
+  int waves;             // wavefronts of a workgroup of the kernel for few rows: 4 or 8
   int rows_over, rows_to;  // the launch takes sequences of more rows than the one, up to the other
 };
 // 16-row tiles of a workgroup of the kernel for many rows

@@ -1050,12 +1050,10 @@ __device__ __forceinline__ void join_parts(const Kv4AttnArgs& a, const Tile& t, 
 }
 
 // ---- attention of few rows over long caches -------------------------------------------------
-// Wavefronts take a piece's steps in turn and join their sums through LDS.
-constexpr int ROWS_WAVES = 8;
-
-template <int D, int FMT, int NT>
-__global__ __launch_bounds__(64 * ROWS_WAVES, 2) void kv4_attn_rows_kernel(Kv4AttnArgs a) {
-  constexpr int R = 16 * NT, LD = D + 4, NW = ROWS_WAVES, SIZE = R * (D + 2);
+// NW (4 or 8) wavefronts take a piece's steps in turn and join their sums through LDS.
+template <int D, int FMT, int NT, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void kv4_attn_rows_kernel(Kv4AttnArgs a) {
+  constexpr int R = 16 * NT, LD = D + 4, SIZE = R * (D + 2);
   __shared__ float lds_o[NW][16][LD];
   __shared__ float lds_m[NW][R], lds_l[NW][R];
   __shared__ int lds_flag;
@@ -1098,8 +1096,8 @@ __global__ __launch_bounds__(64 * ROWS_WAVES, 2) void kv4_attn_rows_kernel(Kv4At
     first_round = false;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      // the two wavefronts of a SIMD go first in turn: left alone, the older one always does, and
-      // the other ends 4 us behind it
+      // the wavefronts of a SIMD go first in turn: left alone, the older one always does, and the
+      // other ends 4 us behind it (wavefronts of several workgroups: 3 to 5 % in all)
       if ((i ^ (wave >> 2)) & 1)
         __builtin_amdgcn_s_setprio(1);
       else
@@ -1783,13 +1781,14 @@ hipError_t launch_attn(const Kv4AttnArgs& a, hipStream_t st) {
     kv4_attn_tiles_kernel<D, FMT><<<grid, TILE_THREADS, 0, st>>>(a);
     return hipGetLastError();
   }
+  const auto rows = [&](auto kernel) { kernel<<<grid, 64 * a.waves, 0, st>>>(a); };
   if constexpr (D <= 128) {
     if (a.nt == 2) {
-      kv4_attn_rows_kernel<D, FMT, 2><<<grid, 64 * ROWS_WAVES, 0, st>>>(a);
+      rows(a.waves == 4 ? kv4_attn_rows_kernel<D, FMT, 2, 4> : kv4_attn_rows_kernel<D, FMT, 2, 8>);
       return hipGetLastError();
     }
   }
-  kv4_attn_rows_kernel<D, FMT, 1><<<grid, 64 * ROWS_WAVES, 0, st>>>(a);
+  rows(a.waves == 4 ? kv4_attn_rows_kernel<D, FMT, 1, 4> : kv4_attn_rows_kernel<D, FMT, 1, 8>);
   return hipGetLastError();
 }
 template <template <int, int> class L, class A>

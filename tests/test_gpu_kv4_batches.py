@@ -40,6 +40,18 @@ def test_long_caches_among_many_sequences(fmt, D, window):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("D,H,rows,long", [(64, 4, 1, 0), (128, 2, 1, 0), (128, 2, 4, 2600),
+                                           (256, 2, 1, 2100), (256, 8, 1, 0)])
+def test_many_tiles(fmt, D, H, rows, long):
+    """Tiles enough for the workgroups of fewer wavefronts; one long cache is cut all the same."""
+    B = 800 // H
+    r, lens = ragged(B, rows, 70, D)
+    if long:
+        r[B // 2], lens[B // 2] = rows, long
+    attention_case(r, lens, D, H, 2, fmt, 32, 32, seed=D + H, window=long // 2, sinks=3)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("B", [65, 700, 4100])
 def test_rows_of_many_sequences(fmt, B):
     b = _b()
