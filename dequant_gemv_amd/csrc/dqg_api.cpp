@@ -372,6 +372,10 @@ int check_kv4_rows(const void* p, int64_t stride, int heads, int D) {
   if (stride < (int64_t)heads * D || stride > ((int64_t)1 << 32)) return DQG_ERR_INVALID_ARG;
   return aligned16(p) && stride % 8 == 0 ? DQG_OK : DQG_ERR_MISALIGNED;
 }
+// (a grid has fewer than 2^32 threads: 64 for K and 64 for V of a block of 8 rows and head)
+bool kv4_rows_fit(int T, int B, int Hkv) {
+  return 2 * (long long)Hkv * (T / 8 + 2 * (long long)B) < (1LL << 26) - 4;
+}
 dqg::Kv4Where kv4_where(int T, int B, const int32_t* cu, const int32_t* lens, const int32_t* table,
                         int max_pages, const uint8_t* cache, int num_pages, int Hkv, int D,
                         int page_size, int group, int* status) {
@@ -701,6 +705,7 @@ int kv4_write(const uint16_t* k, const uint16_t* v, int T, int64_t k_stride, int
                            D, page_size, group, format, status);
   if (rc == DQG_OK) rc = check_kv4_rows(k, k_stride, Hkv, D);
   if (rc == DQG_OK) rc = check_kv4_rows(v, v_stride, Hkv, D);
+  if (rc == DQG_OK && !kv4_rows_fit(T, B, Hkv)) rc = DQG_ERR_UNSUPPORTED;
   if (rc != DQG_OK) return rc;
   dqg::Kv4RowsArgs a{};
   a.w = kv4_where(T, B, cu_rows, kv_lens, block_table, max_pages, cache, num_pages, Hkv, D,
@@ -717,6 +722,7 @@ int kv4_read(uint16_t* k, uint16_t* v, int T, int64_t k_stride, int64_t v_stride
                            D, page_size, group, format, status);
   if (rc == DQG_OK) rc = check_kv4_rows(k, k_stride, Hkv, D);
   if (rc == DQG_OK) rc = check_kv4_rows(v, v_stride, Hkv, D);
+  if (rc == DQG_OK && !kv4_rows_fit(T, B, Hkv)) rc = DQG_ERR_UNSUPPORTED;
   if (rc != DQG_OK) return rc;
   dqg::Kv4RowsArgs a{};
   a.w = kv4_where(T, B, cu_rows, kv_lens, block_table, max_pages, cache, num_pages, Hkv, D,
@@ -807,11 +813,17 @@ int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32
     a.plan = cut && B > 64 ? reinterpret_cast<int2*>(ws + kKv4CounterBytes + kv4_partial_bytes(Hkv, D))
                            : nullptr;
     a.n_groups = (int)(tiles + (cut ? a.n_parts : 0));
-    if ((long long)a.n_groups * Hkv >= (1LL << 31)) return DQG_ERR_UNSUPPORTED;
     return dqg::launch_kv4_attention(a, D, format, stream) == hipSuccess ? DQG_OK : DQG_ERR_HIP;
   };
+  // a grid has fewer than 2^32 threads, a workgroup up to 512
+  const auto fits = [&](int tiles16) {
+    return ((long long)T * a.r / (16 * tiles16) + B + kv4_parts(Hkv)) * Hkv < (1LL << 23);
+  };
   const int few = kKv4FewRows / a.r;  // rows of a sequence that are few
+  if (!fits(nt_many)) return DQG_ERR_UNSUPPORTED;
   if (force == DQG_KV4_FORCE_MANY) return launch(nt_many, 0, INT_MAX);
+  if (!fits(nt))
+    return rows <= few || force ? DQG_ERR_UNSUPPORTED : launch(nt_many, 0, INT_MAX);
   if (rows <= few || force == DQG_KV4_FORCE_FEW) return launch(nt, 0, INT_MAX);
   const int R = 16 * nt, RM = 16 * nt_many, i = D == 64 ? 0 : D == 128 ? 1 : 2;
   const double step_few[3] = {1.1, 1.5, 1.3}, step_many[3] = {1.3, 2.2, 2.8};  // by head dim

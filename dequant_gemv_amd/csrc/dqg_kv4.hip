@@ -836,7 +836,9 @@ __device__ __forceinline__ bool set_piece(const Kv4AttnArgs& a, int at, int tile
   f.s0 = f.index * chunk;
   f.s1 = min(f.s0 + chunk, steps);
   // (always so for cu_rows that ascend)
-  return f.tile >= 0 && f.tile < tiles && (f.n == 1 || (unsigned)f.partial < 2u * a.n_parts);
+  const int first = f.partial - f.index;
+  return f.tile >= 0 && f.tile < tiles &&
+         (f.n == 1 || (first >= 0 && first <= 2 * a.n_parts - f.n));
 }
 // The x-th piece, from the last (the pieces of later tiles, which see more, first); false: there
 // are not as many.  Uniform over the workgroup.

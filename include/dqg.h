@@ -375,10 +375,14 @@ int packed_gemv_int4_tiled(const uint16_t* x, int T, int K, int N, const uint8_t
  *               positions beyond likewise).  The caller clears it.
  * All of cu_rows, kv_lens and block_table are read on the device.  Limits: D in {64, 128, 256},
  * G in {32, 128} dividing D, page_size a power of two from 32 to 65536, max_pages * page_size
- * <= 2^30, B <= 65536, T <= 2^22, Hkv <= 1024.  cache and the row tensors 16-byte aligned, row
- * strides (in elements) multiples of 8 and at least heads * D: rows may be columns of a wider
- * matrix.  Two sequences that own rows of one kv4_write call must not share the pages that
- * these rows fall into.
+ * <= 2^30, B <= 65536, T <= 2^22, Hkv <= 1024, (T / 8 + 2 B) Hkv < 2^25 (writing and reading),
+ * (T Hq / (16 Hkv) + B + 256) Hkv < 2^23 (attention).  cache and the row tensors 16-byte aligned,
+ * row strides (in elements) multiples of 8 and at least heads * D: rows may be columns of a wider
+ * matrix.  The rows of one kv4_write call must fall into different places: sequences that own
+ * rows do not share the pages that these fall into, nor does one sequence's table name such a
+ * page twice.  (cu_rows that do not ascend give rows nobody can predict, and may leave a
+ * workspace that has to be zero-filled again; like all values read on the device they lead to no
+ * access outside the tensors.)
  */
 
 /* Host only: bytes of one page, Hkv * page_size * (D + 4 D / G).  0 for unsupported sizes. */
@@ -388,9 +392,9 @@ size_t kv4_page_bytes(int Hkv, int D, int page_size, int group);
  * kv4_write -- quantises rows k and v (bf16 [T, Hkv, D]) into the cache.  Per row, head and group
  * of G values x: a = max |x|; scale = bf16_rne(a / 7) (INT4) or bf16_rne(a / 6) (FP4), 0 where
  * a < 2^-100, NaN where the group holds a NaN or an infinity (it reads back as NaN); code = the
- * nearest of x / scale, ties to the even code (FP4: with the sign of x, also of zeros).  Exactly these codes on every call: the result
- * does not depend on T or on the rows' grouping into calls.  Positions that the call does not
- * write keep their values.
+ * nearest of x / scale, ties to the even code (FP4: with the sign of x, also of zeros).  Exactly
+ * these codes on every call: the result does not depend on T or on the rows' grouping into calls.
+ * Positions that the call does not write keep their values.
  */
 int kv4_write(const uint16_t* k, const uint16_t* v, int T, int64_t k_stride, int64_t v_stride,
               int B, const int32_t* cu_rows, const int32_t* kv_lens, const int32_t* block_table,

@@ -96,6 +96,19 @@ def test_attention_is_refused(kw, status):
     assert _attend(**kw) == status
 
 
+@pytest.mark.parametrize("fn", ["kv4_write", "kv4_read"])
+@pytest.mark.parametrize("T,B_,H", [(1 << 22, 1, 1024), (1, 65536, 256), (1 << 22, 65536, 52)])
+def test_rows_beyond_a_grid_are_refused(fn, T, B_, H):
+    assert _rows(fn, T=T, B=B_, H=H, ks=H * 128, vs=H * 128) == UNS
+
+
+@pytest.mark.parametrize("T,B_,Hq,H,path", [
+    (65536, 65536, 128, 128, 0), (1 << 18, 65536, 1024, 128, B.KV4_FORCE_FEW),
+    (1 << 16, 65536, 1024, 1024, B.KV4_FORCE_MANY), (1 << 16, 1 << 16, 128, 128, B.KV4_FORCE_FEW)])
+def test_tiles_beyond_a_grid_are_refused(T, B_, Hq, H, path):
+    assert _attend(T=T, B=B_, Hq=Hq, H=H, qs=Hq * 128, os=Hq * 128, fmt=path) == UNS
+
+
 def test_binding_refuses():
     c = torch.zeros(3, B.kv4_page_bytes(2, 64, 32, 32), dtype=torch.uint8)
     cu, lens = torch.zeros(2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
