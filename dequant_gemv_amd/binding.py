@@ -565,8 +565,8 @@ def kv4_attention(q, cu_rows, kv_lens, block_table, cache, kv_heads: int, page_s
         _need_flat(lse, "lse", torch.float32, (T, H), dev)
     if workspace is not None:
         _need_flat(workspace, "workspace", torch.uint8, workspace.shape, dev)
-    _call("kv4_attention", LIB.kv4_attention, dev, q.data_ptr(), T, qs, B, cu_rows.data_ptr(), kv_lens.data_ptr(),
-          block_table.data_ptr(), mp, cache.data_ptr(), pages, H, kv_heads, D, page_size, group,
+    _call("kv4_attention", LIB.kv4_attention, dev, q.data_ptr(), T, qs, B, cu_rows.data_ptr(),
+          kv_lens.data_ptr(), block_table.data_ptr(), mp, cache.data_ptr(), pages, H, kv_heads, D, page_size, group,
           fmt, scale, window, sinks, max_rows, max_kv_len, out.data_ptr(), os_, _addr(lse),
           _addr(status), _addr(workspace), 0 if workspace is None else workspace.numel())
     return out

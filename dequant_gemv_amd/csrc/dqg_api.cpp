@@ -800,8 +800,9 @@ int kv4_attention(const uint16_t* q, int T, int64_t q_stride, int B, const int32
     a.min_steps = min_steps;
     a.waves = Hkv * tiles_of(R) >= (D == 64 ? 3 : 2) * kKv4Resident ? 4 : 8;
     // (hints may be wrong: any n_parts gives the right result)
-    a.n_parts = (int)std::max(1LL, std::min<long long>(kv4_parts(Hkv), (tiles_of(R) * steps_of(R) + min_steps - 1) /
-                                                                           min_steps));
+    a.n_parts = (int)std::max(
+        1LL, std::min<long long>(kv4_parts(Hkv),
+                                 (tiles_of(R) * steps_of(R) + min_steps - 1) / min_steps));
     // sum of ceil(n r / R) over the sequences; pieces are at most tiles + parts
     const long long tiles = (long long)T * a.r / R + B;
     // places in a batch's steps are 32-bit

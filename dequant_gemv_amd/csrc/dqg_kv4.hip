@@ -198,8 +198,9 @@ struct Layout {
 // fill keeps the other positions' nibbles.  A wavefront takes K or V of one block and head: the
 // most wavefronts, for a single row as for a prompt.
 // Instructions bound it, not memory (per wavefront about 250 for K, 450 for V and 2 KB of rows):
-// maxima cross lanes by DPP, loads and scales are free of branches.  3 times 5001 rows of 4 heads
-// of 128: 10.2 us (39 MB: 3.8 TB/s, of the 5.1 of a large copy); one row: 3.6 us.
+// maxima cross lanes by DPP, loads and scales are free of branches.  12171 rows of 4 heads of 128 in
+// 3 prompts: 10.2 us (32 MB: 3.1 TB/s, of the 5.1 of a large copy; with branches and LDS exchanges
+// 13.2); one row: 3.5 us.
 template <int D, int FMT>
 __global__ __launch_bounds__(256) void kv4_write_kernel(Kv4RowsArgs a, int n_units) {
   const int unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -327,7 +328,7 @@ __global__ __launch_bounds__(256) void kv4_write_kernel(Kv4RowsArgs a, int n_uni
 // ---- read ---------------------------------------------------------------------------------
 // The same lanes the other way round.  Rows without a place in the cache (before position 0, or
 // behind the table, or in a page that is not there) read as zeros.  Bound by memory: 32768 rows of
-// 4 heads of 128 17.0 us (86 MB: 5.1 TB/s, as a large copy); the 15003 rows above 9.4 us.
+// 4 heads of 128 16.7 us (86 MB: 5.1 TB/s, as a large copy); the 12171 rows above 9.3 us.
 template <int D, int FMT>
 __global__ __launch_bounds__(256) void kv4_read_kernel(Kv4RowsArgs a, int n_units) {
   const int unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -790,7 +791,8 @@ __device__ __forceinline__ float row_lse(float m, float l) {
 // once (or than the tiles), so that ragged batches, single long caches and many short ones load
 // the GPU evenly in one round.  (Cutting the steps of all tiles, end to end, into equal parts
 // loads it more evenly still, but parts that reach over two tiles pay a workgroup's start and end
-// twice, 8 us: 8 sequences of up to 4099 positions and 4 rows took 28 us, 32 of up to 8192 31 us.)
+// twice, 8 us: 8 sequences of up to 4099 positions and 4 rows took 28 us that way and take 20, 32
+// of up to 8192 took 31 and take 30.)
 // The pieces of a cut tile leave partial sums, and the workgroup that finishes last joins them in
 // order of position.
 // Tiles of a sequence and (an upper bound of) the steps of each; a tile that sees nothing counts
@@ -843,9 +845,9 @@ __device__ __forceinline__ bool set_piece(const Kv4AttnArgs& a, int at, int tile
 // The x-th piece, from the last (the pieces of later tiles, which see more, first); false: there
 // are not as many.  Uniform over the workgroup.
 // Up to 64 sequences: one a lane.  More: from the plan that a kernel before this one has made (as
-// many loads as a search needs, where every workgroup would go through the whole batch), or,
-// where nothing is cut, by slots: floor(cu[b + 1] r / R) - floor(cu[b] r / R) + 1 are enough for
-// the tiles of sequence b.
+// many loads as a search needs; every workgroup going through the whole batch took 7.5 ms where
+// 4096 single tokens of 8 kv heads take 0.8), or, where nothing is cut, by slots:
+// floor(cu[b + 1] r / R) - floor(cu[b] r / R) + 1 are enough for the tiles of sequence b.
 __device__ __forceinline__ bool find_piece(const Kv4AttnArgs& a, int R, int x, Piece& f) {
   int tiles, steps, chunk;
   if (a.w.B > 64) {
@@ -1052,7 +1054,15 @@ __device__ __forceinline__ void join_parts(const Kv4AttnArgs& a, const Tile& t, 
 }
 
 // ---- attention of few rows over long caches -------------------------------------------------
-// NW (4 or 8) wavefronts take a piece's steps in turn and join their sums through LDS.
+// NW (4 or 8) wavefronts take a piece's steps of 32 positions in turn and join their sums through
+// LDS; codes go from memory to registers to matrix operands, each read once.  The next step's codes
+// are loaded behind the arithmetic of this one (two steps ahead gained nothing, 128 registers for
+// 4 wavefronts a SIMD spilled).
+// Measured: a single cache of 131072 positions, 4 kv heads of 128: 23 us, of which the loop takes
+// 13 at 5.8 TB/s; the rest is a workgroup's chain of dependent steps: start 2 to 4 us (workgroups
+// are started one after the other), finding its piece 2, table and first codes 1.3, joining
+// wavefronts 2, joining 64 parts 4.  A batch of 32 such heads' caches of up to 8192: 30 us (97 MB);
+// 1000 positions of one sequence: 10 us, all of it that chain.
 template <int D, int FMT, int NT, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void kv4_attn_rows_kernel(Kv4AttnArgs a) {
   constexpr int R = 16 * NT, LD = D + 4, SIZE = R * (D + 2);
@@ -1221,6 +1231,12 @@ __global__ __launch_bounds__(64 * NW, 2) void kv4_attn_rows_kernel(Kv4AttnArgs a
 // its share.  (K of turn t + 1 takes the place of turn t - 1's, last read in slot 2 t - 1, and is
 // first read in slot 2 t + 2; V of turn t that of turn t - 2's, last read in slot 2 t - 1, first
 // read in slot 2 t + 2.)
+//
+// Bound by matrix instructions together with the arithmetic between them (a SIMD overlaps the two of
+// different wavefronts only in part): two causal prompts of 4096 rows, 32 heads of 128, 220 us in a
+// row (870 TFLOP/s; a large matrix product reaches 1150), 250 after other work; a prompt of 8192
+// rows, 16 heads of 256, window 1024, 210 us (615 TFLOP/s).  Interleaving the two kinds by hand in one
+// wavefront spilled and took 373 us; the two phases of D = 256 took 305 for heads of 128.
 constexpr int TILE_POS = 64, TILE_THREADS = 512, K_STRIDE = TILE_POS + 1;
 __host__ __device__ constexpr int tile_halves(int D) { return D > 128 ? 2 : 1; }
 __host__ __device__ constexpr int tile_rows(int D) { return 16 * kv4_tile_nt(D); }
@@ -1479,7 +1495,8 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
   uint32_t scales = 0;
   const auto go_to = [&](int turn) {
     const int i = s0 + 2 * turn + group - list0;
-    codes = a.w.cache + (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(l_codes >> 32), i) << 32) |
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(l_codes >> 32), i);
+    codes = a.w.cache + (int64_t)((uint64_t)hi << 32 |
                                   (uint32_t)__builtin_amdgcn_readlane((int)l_codes, i));
     scales = (uint32_t)__builtin_amdgcn_readlane(l_scales, i);
   };
