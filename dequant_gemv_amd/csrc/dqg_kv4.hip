@@ -669,10 +669,15 @@ __device__ __forceinline__ void step_scores(const KStage<D>& x, const Queries<D,
     for (int h = 0; h < 2; ++h) sc[nt][h] *= c;
 }
 
+// largest scale whose values and decode constants (INT4: 24 s) are finite in fp16, as bf16 bits
+__host__ __device__ constexpr uint32_t scale_limit(int fmt) {
+  return fmt == FMT_INT4 ? 0x452Au : 0x462Au;
+}
+
 // Steps with positions that some row does not see.  What lies there may be anything: scores are
-// replaced and V scales cleared.  A position whose V scale is not finite and that only some rows
+// replaced and V scales cleared.  A position whose V scale fp16 cannot take and that only some rows
 // see is cleared too, and the rows that see it get a NaN score.
-template <int D, int NT>
+template <int D, int FMT, int NT>
 __device__ __forceinline__ void step_mask(const Kv4AttnArgs& a, const Tile& t, int t0, int g,
                                           const Queries<D, NT>& q, f32x4_t (&sc)[NT][2],
                                           uint4 (&vs)[D / 64]) {
@@ -688,7 +693,7 @@ __device__ __forceinline__ void step_mask(const Kv4AttnArgs& a, const Tile& t, i
 #pragma unroll
     for (int e = 0; e < D / 64; ++e) {
       const uint32_t b16 = (i & 1) ? vw[e][i / 2] >> 16 : vw[e][i / 2] & 0xFFFFu;
-      bad |= (b16 & 0x7F80u) == 0x7F80u;
+      bad |= (b16 & 0x7FFFu) > scale_limit(FMT);
     }
     const uint64_t bads = __ballot(bad);
     const bool poisoned = ((bads >> (16 * g)) & 0xFFFFu) != 0;
@@ -1117,7 +1122,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kv4_attn_rows_kernel(Kv4AttnArgs a
       if (page >= 0) {
         f32x4_t sc[NT][2];
         step_scores<D, FMT, NT>(ks, q, c, sc);
-        if (step_at_edge(a, t, t0)) step_mask<D, NT>(a, t, t0, g, q, sc, vs.s);
+        if (step_at_edge(a, t, t0)) step_mask<D, FMT, NT>(a, t, t0, g, q, sc, vs.s);
         f16x8_t p[NT];
         step_weights<D, FMT, NT>(sc, acc, p);
         step_values<D, FMT, NT>(vs, p, acc);
@@ -1241,9 +1246,6 @@ constexpr int TILE_POS = 64, TILE_THREADS = 512, K_STRIDE = TILE_POS + 1;
 __host__ __device__ constexpr int tile_halves(int D) { return D > 128 ? 2 : 1; }
 __host__ __device__ constexpr int tile_rows(int D) { return 16 * kv4_tile_nt(D); }
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
-
-// largest scale whose values and decode constants (INT4: 24 s) are finite in fp16, as bf16 bits
-__host__ __device__ constexpr uint32_t scale_limit(int fmt) { return fmt == FMT_INT4 ? 0x452Au : 0x462Au; }
 
 // halves of a dword of V scales that are above the limit, as nonzero halves
 template <int FMT>

@@ -197,3 +197,27 @@ def test_largest_window_and_sinks():
             want = bits16(call(None, **path_kw))
             for window, sinks in ((TOP, 0), (TOP, TOP), (1, TOP), (2 ** 30, 3)):
                 assert np.array_equal(bits16(call(None, window=window, sinks=sinks, **path_kw)), want)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("bits", [0x452B, 0x462B, 0x4700, 0x7F7F, 0xC700])
+def test_hidden_values_beyond_the_range_do_not_leak(fmt, bits):
+    """A finite scale that fp16 products cannot take: rows that do not see its position are clean."""
+    b = _b()
+    D, page, n, at = 128, 32, 100, 37
+    for what in ("k", "v"):
+        for window in (0, 20):
+            cu, lens, table, pages, T = U.batch([n], [n], page)
+            c = U.random_cache(pages, 1, D, page, 32, fmt, held=U.held_of(lens, table, page))
+            _, ks, _, vs = c._off(0, at % page)
+            place = (int(table[0, at // page]), ks if what == "k" else vs)
+            c._put_scale(*place, bits)
+            q = K.bf16_value(U.bf16_bits(np.random.default_rng(1).normal(size=(n, 2, D))))
+            args = (rows_dev(q), *call_where(c, cu, lens, table, fmt), 1, page, 32)
+            sees = np.array([p >= at and (window == 0 or at > p - window) for p in range(n)])
+            c._put_scale(*place, 0)
+            want, lse, slack = K.attention(c, q, cu, lens, table, fmt, 0.125, window)
+            bound, _ = U.attention_bounds((want, lse), slack, D)
+            for path in (b.KV4_FORCE_FEW, b.KV4_FORCE_MANY):
+                got = bf16_f64(bits16(b.kv4_attention(*args, fmt | path, 0.125, window=window)))
+                assert np.all(np.abs(got - want)[~sees] <= bound[~sees]), (what, window, path)
