@@ -1214,7 +1214,7 @@ __global__ __launch_bounds__(64 * NW, 2) void kv4_attn_rows_kernel(Kv4AttnArgs a
 // ---- attention of many rows -------------------------------------------------------------------
 // A workgroup of 8 wavefronts walks the visible positions 64 at a time (a turn).  The codes are
 // decoded once for all its rows, into LDS:
-//   K: [D / 8][65] units of 16 bytes (8 d of one position; 65: banks), V: [8][D] units (8 positions
+//   K: [D / 8][64] units of 16 bytes (8 d of one position; see k_unit), V: [8][D] units (8 positions
 //   of one d).  Both are the A operands of 32x32x16 matrix instructions as they lie.
 //   S^T = K Q^T, O^T += V^T P^T as above; row m of a 32-position A operand is position
 //   16 (m / 16) + 8 ((m / 4) % 2) + 4 ((m % 16) / 8) + m % 4, so that lane (q, h) ends up with
@@ -1242,7 +1242,10 @@ __global__ __launch_bounds__(64 * NW, 2) void kv4_attn_rows_kernel(Kv4AttnArgs a
 // row (870 TFLOP/s; a large matrix product reaches 1150), 250 after other work; a prompt of 8192
 // rows, 16 heads of 256, window 1024, 210 us (615 TFLOP/s).  Interleaving the two kinds by hand in one
 // wavefront spilled and took 373 us; the two phases of D = 256 took 305 for heads of 128.
-constexpr int TILE_POS = 64, TILE_THREADS = 512, K_STRIDE = TILE_POS + 1;
+constexpr int TILE_POS = 64, TILE_THREADS = 512;
+// where the units of 8 d's positions start: those that 8 threads write at once lie 2 units apart
+// (modulo the 16 that the banks hold), so that 64 threads' units spread evenly
+__host__ __device__ constexpr int k_unit(int D, int u) { return TILE_POS * u + 2 * (u / (D / 64)); }
 __host__ __device__ constexpr int tile_halves(int D) { return D > 128 ? 2 : 1; }
 __host__ __device__ constexpr int tile_rows(int D) { return 16 * kv4_tile_nt(D); }
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
@@ -1330,7 +1333,7 @@ __device__ __forceinline__ void tile_scores(const uint4* k, const f16x8_t (&q)[D
   constexpr int J = 4 / NU, G = D / 16 / J;  // groups of 4 operands: J times 16 d
   const auto read = [&](int n, uint4 (&x)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = k[2 * (J * n + i / NU) * K_STRIDE + 32 * (i % NU)];
+    for (int i = 0; i < 4; ++i) x[i] = k[k_unit(D, 2 * (J * n + i / NU)) + 32 * (i % NU)];
   };
   uint4 x[2][4];
   read(0, x[0]);
@@ -1434,7 +1437,7 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
   constexpr int HV = tile_halves(D), R = tile_rows(D), NU = 2 / HV, N = D / 64, NJ = D / 32 / HV;
   constexpr int NE = TileStage<D>::NE, SIZE = R * (D + 2);
   constexpr int NOWHERE = 0x40000000;  // place of a step that is not there: behind every row
-  __shared__ uint4 lds_k[2][D / 8][K_STRIDE];
+  __shared__ uint4 lds_k[2][k_unit(D, D / 8)];
   __shared__ uint4 lds_v[2][TILE_POS / 8][D];
   __shared__ uint32_t lds_bad[4][8];  // positions of each block whose V scale is not usable
   __shared__ uint4 lds_p[HV == 2 ? 4 : 1][HV == 2 ? 4 : 1][64];
@@ -1510,7 +1513,7 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
     const f16x2_t s4[4] = {s, s, s, s}, z4[4] = {s24, s24, s24, s24};
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      lds_k[turn & 1][map.kd + i][map.tok] =
+      lds_k[turn & 1][k_unit(D, map.kd + i) + map.tok] =
           __builtin_bit_cast(uint4, decode_f16<FMT>(st.k[i], s4, z4));
 #pragma unroll
     for (int e = 0; e < NE; ++e) {
@@ -1674,7 +1677,7 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
         __builtin_amdgcn_s_setprio(1);
         if (group == 1) decode_next(turn + 1);
         __builtin_amdgcn_s_setprio(0);
-        tile_scores<D, NU>(&lds_k[turn & 1][h][k_tok], q, sc);
+        tile_scores<D, NU>(&lds_k[turn & 1][k_unit(D, h) + k_tok], q, sc);
         const float ref = move_reference(mask_scores(turn));
         __builtin_amdgcn_s_setprio(1);
         tile_values<D, NJ>(&lds_v[turn & 1][h][q32], [&](int b) { return weights(b, ref); }, o);
@@ -1718,7 +1721,7 @@ __global__ __launch_bounds__(TILE_THREADS, 2) void kv4_attn_tiles_kernel(Kv4Attn
       // phase M
       __builtin_amdgcn_s_setprio(1);
       if (turn > 0) values(turn - 1);
-      tile_scores<D, NU>(&lds_k[turn & 1][h][32 * half + k_tok], q, sc);
+      tile_scores<D, NU>(&lds_k[turn & 1][k_unit(D, h) + 32 * half + k_tok], q, sc);
       __builtin_amdgcn_s_setprio(0);
       float mx = mask_scores(turn);
       mx = fmaxf(mx, __shfl_xor(mx, 32));
