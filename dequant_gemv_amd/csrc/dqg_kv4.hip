@@ -1243,9 +1243,13 @@ __global__ __launch_bounds__(64 * NW, 2) void kv4_attn_rows_kernel(Kv4AttnArgs a
 // rows, 16 heads of 256, window 1024, 210 us (615 TFLOP/s).  Interleaving the two kinds by hand in one
 // wavefront spilled and took 373 us; the two phases of D = 256 took 305 for heads of 128.
 constexpr int TILE_POS = 64, TILE_THREADS = 512;
-// where the units of 8 d's positions start: those that 8 threads write at once lie 2 units apart
-// (modulo the 16 that the banks hold), so that 64 threads' units spread evenly
-__host__ __device__ constexpr int k_unit(int D, int u) { return TILE_POS * u + 2 * (u / (D / 64)); }
+// where the units of 8 d's positions start: those that 8 threads write at once (D / 64 rows of
+// units apart) lie 1 or 2 units apart modulo the 16 that the banks hold, so that a wavefront's units
+// spread.  (256: rows 65 apart put them on 4 of the 16; 128: 2 padding units for 2 rows took 1 to
+// 3 % longer.)
+__host__ __device__ constexpr int k_unit(int D, int u) {
+  return TILE_POS * u + (D > 128 ? 2 * (u / 4) : u);
+}
 __host__ __device__ constexpr int tile_halves(int D) { return D > 128 ? 2 : 1; }
 __host__ __device__ constexpr int tile_rows(int D) { return 16 * kv4_tile_nt(D); }
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
